@@ -2,7 +2,9 @@
 
 The computation lives in the HIP library ``liblapnys.so`` (C ABI in
 ``include/lapnys.h``); ``laplacian_nystr_approximation_amd.lapnys`` is its
-ctypes binding, whose names are re-exported here.  The library is loaded on
+ctypes binding, whose names are re-exported here, and so are those of
+``laplacian_nystr_approximation_amd.lapmix``, the binding of the operators beside
+the attention (``include/lapmix.h``).  The library is loaded on
 first use of any of them, and that use raises ImportError if it has not been
 built (``python -m laplacian_nystr_approximation_amd.build``).
 """
@@ -17,8 +19,17 @@ _BINDING_NAMES = {
     "lapnys_forward_noalloc",
 }
 
+_MIX_NAMES = {
+    "lapmix_scan_params", "lapmix_norm_params", "make_scan_params", "make_norm_params",
+    "lapmix_scan_workspace_size", "lapmix_scan_states_size", "lapmix_scan_forward_ws", "lapmix_scan_backward_ws",
+    "lapmix_scan_step", "lapmix_norm_forward", "lapmix_norm_workspace_size", "lapmix_norm_backward_ws",
+    "LAPMIX_SCAN_TILE",
+}
+
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         return getattr(importlib.import_module(".lapnys", __name__), name)
+    if name in _MIX_NAMES:
+        return getattr(importlib.import_module(".lapmix", __name__), name)
     raise AttributeError(name)

@@ -40,7 +40,7 @@ def sanitizer_runtime() -> str | None:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.hpp"))
-                  + [os.path.join(INCLUDE, "lapnys.h")])
+                  + [os.path.join(INCLUDE, h) for h in ("lapnys.h", "lapmix.h")])
 
 
 def stale() -> bool:

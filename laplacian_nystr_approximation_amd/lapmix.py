@@ -1,0 +1,237 @@
+"""ctypes binding of the lapmix operators (include/lapmix.h): argument marshalling only.
+
+The gated linear recurrence (``lapmix_scan_*``) and the root-mean-square norm
+with the residual's addition (``lapmix_norm_*``), in the manner of the attention's
+binding: functions carry the names of the C entry points, outputs are given by the
+caller, tensors are device tensors of the current device, and a negative status
+raises ``LapnysError``.  [B, H, N, d] tensors may be views with any strides as long
+as channels are contiguous (a permuted [B, N, H, d] tensor, a slice of a projection):
+the binding passes their strides.  Plain integers are raw device pointers, with the
+strides that the params hold.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .lapnys import LAPNYS_BF16, LAPNYS_F32, _check, _lib, _ptr, _stream, _ws
+
+LAPMIX_E4M3 = 2
+LAPMIX_GATE_LOG = 1
+LAPMIX_COUPLED = 2
+LAPMIX_SCAN_TILE = 256
+
+_SIZES = {LAPNYS_F32: 4, LAPNYS_BF16: 2, LAPMIX_E4M3: 1}
+_NAMES = {"f32": LAPNYS_F32, "bf16": LAPNYS_BF16, "e4m3": LAPMIX_E4M3}
+_stride = ctypes.c_int64 * 3
+
+
+class lapmix_scan_params(ctypes.Structure):
+    """Mirror of the C struct."""
+
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("x_stride", _stride), ("g_stride", _stride), ("y_stride", _stride)]
+
+
+class lapmix_norm_params(ctypes.Structure):
+    """Mirror of the C struct."""
+
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("r_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("x_stride", _stride)]
+
+
+def _declare():
+    vp, i32, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    S, M = ctypes.POINTER(lapmix_scan_params), ctypes.POINTER(lapmix_norm_params)
+    out = ctypes.POINTER(size)
+    for name, args in {
+        "lapmix_scan_workspace_size": [S, out],
+        "lapmix_scan_states_size": [S, out],
+        "lapmix_scan_forward_ws": [vp, vp, vp, vp, vp, vp, vp, S, vp, size, vp],
+        "lapmix_scan_backward_ws": [vp, vp, vp, vp, vp, vp, vp, vp, vp, S, vp, size, vp],
+        "lapmix_scan_step": [vp, vp, vp, vp, vp, i32, vp, S, vp],
+        "lapmix_norm_forward": [vp, vp, vp, vp, vp, vp, M, vp],
+        "lapmix_norm_workspace_size": [M, out],
+        "lapmix_norm_backward_ws": [vp, vp, vp, vp, vp, vp, vp, M, vp, size, vp],
+    }.items():
+        f = getattr(_lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+
+
+_declare()
+
+
+def make_scan_params(*, B, H, N, d, dtype="f32", gate="sigmoid", coupled=False) -> lapmix_scan_params:
+    """Build a lapmix_scan_params; ``dtype`` is "f32"/"bf16" or the enum value; ``gate`` is "sigmoid"
+    (f = sigmoid(g)) or "log" (f = exp(min(g, 0)), LAPMIX_GATE_LOG); ``coupled`` sets
+    LAPMIX_COUPLED (the input enters as (1 - f) x)."""
+    if gate not in ("sigmoid", "log"):
+        raise ValueError(f"unknown gate {gate!r}")
+    flags = (LAPMIX_GATE_LOG if gate == "log" else 0) | (LAPMIX_COUPLED if coupled else 0)
+    return lapmix_scan_params(B, H, N, d, _NAMES.get(dtype, dtype), flags)
+
+
+def make_norm_params(*, B, H, N, d, x_dtype="f32", r_dtype="f32", y_dtype="f32", eps=1e-6,
+                     group=0) -> lapmix_norm_params:
+    """Build a lapmix_norm_params for B * N rows of H * d columns; types are "f32"/"bf16" (``y_dtype``
+    also "e4m3") or enum values; ``group`` is the columns to a scale (0: one scale a row)."""
+    return lapmix_norm_params(B, H, N, d, _NAMES.get(x_dtype, x_dtype), _NAMES.get(r_dtype, r_dtype),
+                              _NAMES.get(y_dtype, y_dtype), group, eps, 0)
+
+
+def _flat(name, t, size, count):
+    """Pointer of a dense tensor argument that holds at least ``count`` elements of ``size`` bytes."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != size or t.numel() < count:
+        raise ValueError(f"{name}: expected at least {count} elements of {size} bytes, "
+                         f"got {t.numel()} of {t.element_size()}")
+    return _ptr(t)
+
+
+def _heads(name, t, size, p):
+    """(pointer, strides) of a [B, H, N, d] tensor argument; strides None for a raw pointer."""
+    if isinstance(t, int) or t is None:
+        return t, None
+    if t.element_size() != size or t.shape != (p.B, p.H, p.N, p.d):
+        raise ValueError(f"{name}: expected [{p.B}, {p.H}, {p.N}, {p.d}] of {size} bytes, "
+                         f"got {list(t.shape)} of {t.element_size()}")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be device tensors (got a tensor on the host)")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    b, h, n, c = t.stride()
+    if c != 1 and p.d != 1:
+        raise ValueError(f"{name}: channels must be contiguous (stride {c})")
+    # Strides of dimensions of size 1 do not matter; all zero would mean a dense tensor.
+    st = (b if p.B > 1 else 0, h if p.H > 1 else 0, n if p.N > 1 else 0)
+    if not any(st) and p.B * p.H * p.N > 1:
+        raise ValueError(f"{name}: one row repeated for every token is not supported")
+    return t.data_ptr(), st
+
+
+def _agree(name, st, other, of):
+    if st is not None and of is not None and st != of:
+        raise ValueError(f"{name}: expected the strides of {other}, {of}, got {st}")
+
+
+def lapmix_scan_workspace_size(params: lapmix_scan_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.lapmix_scan_workspace_size(ctypes.byref(params), ctypes.byref(n)), "lapmix_scan_workspace_size")
+    return n.value
+
+
+def lapmix_scan_states_size(params: lapmix_scan_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.lapmix_scan_states_size(ctypes.byref(params), ctypes.byref(n)), "lapmix_scan_states_size")
+    return n.value
+
+
+def _scan_params(params, xs, gs, ys):
+    p = lapmix_scan_params.from_buffer_copy(params)
+    if xs is not None:
+        p.x_stride[:] = xs
+    if gs is not None:
+        p.g_stride[:] = gs
+    if ys is not None:
+        p.y_stride[:] = ys
+    return ctypes.byref(p)
+
+
+def lapmix_scan_forward_ws(x, g, y, params: lapmix_scan_params, ws, h0=None, hN=None, states=None, lengths=None,
+                           stream=None) -> None:
+    """y (and the last state hN, and the states that the backward reads) of h_t = f_t h_{t-1} + i_t x_t."""
+    size = _SIZES.get(params.dtype, 0)
+    cols = params.B * params.H * params.d
+    xp, xs = _heads("x", x, size, params)
+    gp, gs = _heads("g", g, size, params)
+    yp, ys = _heads("y", y, size, params)
+    wp, wn = _ws(ws)
+    _check(_lib.lapmix_scan_forward_ws(
+        xp, gp, _flat("h0", h0, 4, cols), _flat("lengths", lengths, 4, params.B), yp, _flat("hN", hN, 4, cols),
+        _flat("states", states, 4, cols * (-(-params.N // LAPMIX_SCAN_TILE))), _scan_params(params, xs, gs, ys), wp, wn,
+        _stream(stream)), "lapmix_scan_forward_ws")
+
+
+def lapmix_scan_backward_ws(x, g, states, dy, dx, dg, params: lapmix_scan_params, ws, dhN=None, dh0=None,
+                            lengths=None, stream=None) -> None:
+    """Gradients of sum(dy * y) + sum(dhN * hN) into dx, dg and dh0; dx and dg have the strides of x and g."""
+    size = _SIZES.get(params.dtype, 0)
+    cols = params.B * params.H * params.d
+    xp, xs = _heads("x", x, size, params)
+    gp, gs = _heads("g", g, size, params)
+    dyp, ys = _heads("dy", dy, size, params)
+    dxp, dxs = _heads("dx", dx, size, params)
+    dgp, dgs = _heads("dg", dg, size, params)
+    _agree("dx", dxs, "x", xs)
+    _agree("dg", dgs, "g", gs)
+    wp, wn = _ws(ws)
+    _check(_lib.lapmix_scan_backward_ws(
+        xp, gp, _flat("states", states, 4, cols * (-(-params.N // LAPMIX_SCAN_TILE))),
+        _flat("lengths", lengths, 4, params.B), dyp, _flat("dhN", dhN, 4, cols), dxp, dgp,
+        _flat("dh0", dh0, 4, cols), _scan_params(params, xs, gs, ys), wp, wn, _stream(stream)),
+        "lapmix_scan_backward_ws")
+
+
+def lapmix_scan_step(x, g, y, h_in, h_out, params: lapmix_scan_params, slots=None, n_slots=None, stream=None) -> None:
+    """One token for every sequence: y = h_out[slot] = f h_in[slot] + i x.  ``h_in`` and ``h_out`` are
+    float32 [n_slots, H, d] pools (``n_slots`` is taken from h_in's shape unless given)."""
+    size = _SIZES.get(params.dtype, 0)
+    if n_slots is None:
+        if isinstance(h_in, int):
+            raise ValueError("n_slots is needed with a raw pool pointer")
+        n_slots = h_in.shape[0]
+    cols = n_slots * params.H * params.d
+    xp, xs = _heads("x", x, size, params)
+    gp, gs = _heads("g", g, size, params)
+    yp, ys = _heads("y", y, size, params)
+    _check(_lib.lapmix_scan_step(
+        xp, gp, _flat("slots", slots, 4, params.B), _flat("h_in", h_in, 4, cols), _flat("h_out", h_out, 4, cols),
+        n_slots, yp, _scan_params(params, xs, gs, ys), _stream(stream)), "lapmix_scan_step")
+
+
+def _norm_params(params, xs):
+    if xs is None:
+        return ctypes.byref(params)
+    p = lapmix_norm_params.from_buffer_copy(params)
+    p.x_stride[:] = xs
+    return ctypes.byref(p)
+
+
+def lapmix_norm_forward(x, w, y, params: lapmix_norm_params, r=None, s=None, scale=None, stream=None) -> None:
+    """s = x + r and y = s / sqrt(mean(s^2) + eps) * w for every token's row (e4m3: with ``scale``)."""
+    p = params
+    C = p.H * p.d
+    n = p.B * p.N * C
+    rs, ysz = _SIZES.get(p.r_dtype, 0), _SIZES.get(p.y_dtype, 0)
+    xp, xs = _heads("x", x, _SIZES.get(p.x_dtype, 0), p)
+    _check(_lib.lapmix_norm_forward(
+        xp, _flat("r", r, rs, n), _flat("w", w, 4, C), _flat("s", s, rs, n), _flat("y", y, ysz, n),
+        _flat("scale", scale, 4, n // (p.group or C)), _norm_params(p, xs), _stream(stream)), "lapmix_norm_forward")
+
+
+def lapmix_norm_workspace_size(params: lapmix_norm_params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.lapmix_norm_workspace_size(ctypes.byref(params), ctypes.byref(n)), "lapmix_norm_workspace_size")
+    return n.value
+
+
+def lapmix_norm_backward_ws(dy, s, w, params: lapmix_norm_params, ws, ds=None, dr=None, dx=None, dw=None,
+                            stream=None) -> None:
+    """Gradients of sum(dy * y) + sum(ds * s) into dr (the stream's), dx (the branch's) and dw."""
+    p = params
+    C = p.H * p.d
+    n = p.B * p.N * C
+    rs = _SIZES.get(p.r_dtype, 0)
+    dxp, xs = _heads("dx", dx, _SIZES.get(p.x_dtype, 0), p)
+    wp, wn = _ws(ws)
+    _check(_lib.lapmix_norm_backward_ws(
+        _flat("dy", dy, _SIZES.get(p.y_dtype, 0), n), _flat("s", s, rs, n), _flat("w", w, 4, C),
+        _flat("ds", ds, rs, n), _flat("dr", dr, rs, n), dxp, _flat("dw", dw, 4, C), _norm_params(p, xs), wp, wn,
+        _stream(stream)), "lapmix_norm_backward_ws")
