@@ -156,7 +156,8 @@ int scan_plan(const lapmix_scan_params* p, lapmix::ScanArgs* a) {
   return LAPNYS_OK;
 }
 
-size_t scan_workspace(const lapmix::ScanArgs&) { return 0; }
+// Rounded up to what workspaces are aligned to.
+size_t workspace_bytes(const lapmix::ScanArgs& a) { return (lapmix::scan_workspace(a) + 255) & ~(size_t)255; }
 
 bool element_aligned(const View& v) { return v.base % (uintptr_t)v.esize == 0; }
 
@@ -175,18 +176,18 @@ int scan_forward(const void* x, const void* g, const float* h0, const int32_t* l
   for (const View& v : all)
     if (!element_aligned(v)) return LAPNYS_ERR_INVALID_ARG;
   if (!distinct(vy)) return LAPNYS_ERR_INVALID_ARG;
-  const size_t need = scan_workspace(a);
-  st = check_workspace(ws, ws_bytes, need);
-  if (st != LAPNYS_OK) return st;
+  const size_t need = workspace_bytes(a);
   const View vws = dense_view(need ? ws : nullptr, (int64_t)need, 1);
   const View out[] = {vy, vhN, vst, vws};
   const View in[] = {vx, vg, h0 == hN ? dense_view(nullptr, 0, 4) : vh0, vlen};
   if (!outputs_apart(out, 4, in, 4) || !disjoint(vh0, vy) || !disjoint(vh0, vst) || !disjoint(vh0, vws))
     return LAPNYS_ERR_INVALID_ARG;
+  st = check_workspace(ws, ws_bytes, need);
+  if (st != LAPNYS_OK) return st;
   a.vec = vec_view(vx) && vec_view(vg) && vec_view(vy);
   a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.y = y, a.hN = hN, a.states = states;
   (void)hipGetLastError();
-  return ok(lapmix::launch_scan_forward(a, s), "recurrence launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;
+  return ok(lapmix::launch_scan_forward(a, ws, s), "recurrence launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;
 }
 
 int scan_backward(const void* x, const void* g, const float* states, const int32_t* lengths, const void* dy,
@@ -206,19 +207,19 @@ int scan_backward(const void* x, const void* g, const float* states, const int32
   for (const View& v : all)
     if (!element_aligned(v)) return LAPNYS_ERR_INVALID_ARG;
   if (!distinct(vdx) || !distinct(vdg)) return LAPNYS_ERR_INVALID_ARG;
-  const size_t need = scan_workspace(a);
-  st = check_workspace(ws, ws_bytes, need);
-  if (st != LAPNYS_OK) return st;
+  const size_t need = workspace_bytes(a);
   const View vws = dense_view(need ? ws : nullptr, (int64_t)need, 1);
   const View out[] = {vdx, vdg, vdh0, vws};
   const View in[] = {vx, vg, vdy, vst, dhN == dh0 ? dense_view(nullptr, 0, 4) : vdhN, vlen};
   if (!outputs_apart(out, 4, in, 6) || !disjoint(vdhN, vdx) || !disjoint(vdhN, vdg) || !disjoint(vdhN, vws))
     return LAPNYS_ERR_INVALID_ARG;
+  st = check_workspace(ws, ws_bytes, need);
+  if (st != LAPNYS_OK) return st;
   a.vec = vec_view(vx) && vec_view(vg) && vec_view(vdy) && vec_view(vdx) && vec_view(vdg);
   a.x = x, a.g = g, a.states = const_cast<float*>(states), a.lengths = lengths;
   a.dy = dy, a.dhN = dhN, a.dx = dx, a.dg = dg, a.dh0 = dh0;
   (void)hipGetLastError();
-  return ok(lapmix::launch_scan_backward(a, s), "recurrence backward launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;
+  return ok(lapmix::launch_scan_backward(a, ws, s), "recurrence backward launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;
 }
 
 int scan_step(const void* x, const void* g, const int32_t* slots, const float* h_in, float* h_out, int32_t n_slots,
@@ -331,14 +332,14 @@ int norm_backward(const void* dy, const void* s, const float* w, const void* ds,
   for (const View& v : all)
     if (!element_aligned(v)) return LAPNYS_ERR_INVALID_ARG;
   if (dx && !distinct(vdx)) return LAPNYS_ERR_INVALID_ARG;
-  st = check_workspace(ws, ws_bytes, need);
-  if (st != LAPNYS_OK) return st;
   const View vws = dense_view(ws, (int64_t)need, 1);
   const View out[] = {vdr, vdx, vdw, vws};
   const View in[] = {vdy, vs, vw, ds == dr ? dense_view(nullptr, 0, 4) : vds};
   if (!outputs_apart(out, 4, in, 4)) return LAPNYS_ERR_INVALID_ARG;
   if (ds && ds == dr && (!disjoint(vds, vdx) || !disjoint(vds, vdw) || !disjoint(vds, vws)))
     return LAPNYS_ERR_INVALID_ARG;
+  st = check_workspace(ws, ws_bytes, need);
+  if (st != LAPNYS_OK) return st;
   a.vec = a.d % 8 == 0 && aligned(dy, 16) && aligned(s, 16) && aligned(w, 16) && aligned(ds, 16) && aligned(dr, 16) &&
           (!dx || (vec_view(vdx) && (a.xs.b | a.xs.h | a.xs.n) % 8 == 0));
   a.dy = dy, a.s = const_cast<void*>(s), a.w = w, a.ds = ds, a.dr = dr, a.dx = dx, a.dw = dw, a.part = (float*)ws;
@@ -355,7 +356,7 @@ int lapmix_scan_workspace_size(const lapmix_scan_params* p, size_t* bytes) {
   lapmix::ScanArgs a;
   const int st = scan_plan(p, &a);
   if (st != LAPNYS_OK) return st;
-  *bytes = scan_workspace(a);
+  *bytes = workspace_bytes(a);
   return LAPNYS_OK;
 }
 

@@ -55,8 +55,10 @@ struct StepArgs {
   void* y;
 };
 
-hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s);
-hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s);
+// Workspace bytes of a forward or backward call (0 where none is needed).
+size_t scan_workspace(const ScanArgs& a);
+hipError_t launch_scan_forward(const ScanArgs& a, void* ws, hipStream_t s);
+hipError_t launch_scan_backward(const ScanArgs& a, void* ws, hipStream_t s);
 hipError_t launch_scan_step(const StepArgs& a, hipStream_t s);
 
 struct NormArgs {
