@@ -310,8 +310,7 @@ int norm_workspace(const lapmix_norm_params* p, lapmix::NormArgs* a, size_t* byt
   const int st = norm_plan(p, a);
   if (st != LAPNYS_OK) return st;
   if (a->y_dtype == LAPMIX_E4M3) return LAPNYS_ERR_UNSUPPORTED;
-  a->parts = lapmix::norm_parts(a->rows, a->C);
-  *bytes = ((size_t)a->parts * a->C * sizeof(float) + 255) & ~(size_t)255;
+  *bytes = (lapmix::norm_part_count(*a) * a->C * sizeof(float) + 255) & ~(size_t)255;
   return LAPNYS_OK;
 }
 

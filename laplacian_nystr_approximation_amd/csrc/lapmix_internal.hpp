@@ -78,8 +78,8 @@ struct NormArgs {
   int parts;
 };
 
-// Row slices of the backward pass, each with one partial sum of dw.
-int norm_parts(long long rows, int C);
+// Partial sums of dw that a backward call may write.
+size_t norm_part_count(const NormArgs& a);
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s);
 

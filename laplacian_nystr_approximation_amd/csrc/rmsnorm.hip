@@ -1,5 +1,12 @@
 // Root-mean-square norm with the residual's addition (include/lapmix.h).
-// One wave takes one row at a time, a column a lane.
+//
+// A row is held in registers by a part of a workgroup, or by all of it: lane i has
+// the chunks i, i + TPR, ... of V neighbouring columns, so x and r are read once,
+// the sum of squares and an e4m3 group's maximum are lane exchanges, and s and y
+// are written from the registers.  The backward pass holds dy, s and ds the same
+// way, the next row's already on their way while a row is worked on; each
+// workgroup takes every gridDim-th row and keeps its part of dw in registers, and
+// a second kernel adds the parts in a fixed order.  Both are bound by HBM.
 #include <type_traits>
 
 #include "lapmix_internal.hpp"
@@ -8,129 +15,388 @@ namespace lapmix {
 
 namespace {
 
-constexpr int kE4M3 = 2;
+constexpr int kNarrow = 256;  // lanes of a workgroup that takes several rows side by side
+constexpr int kWide = 1024;   // most lanes of one that takes a row
 
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// V neighbouring elements as loaded.  V = 8 needs 16-byte alignment.
+template <typename T, int V>
+struct Raw;
+template <typename T>
+struct Raw<T, 1> {
+  T e;
+  __device__ __forceinline__ float operator[](int) const { return widen(e); }
+};
+template <>
+struct Raw<float, 8> {
+  f32x4 lo, hi;
+  __device__ __forceinline__ float operator[](int i) const { return i < 4 ? lo[i] : hi[i - 4]; }
+};
+template <>
+struct Raw<uint16_t, 8> {
+  u32x4 e;
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i % 2 ? e[i / 2] & 0xffff0000u : e[i / 2] << 16);
+  }
+};
+
+template <int V, typename T>
+__device__ __forceinline__ Raw<T, V> get(const T* p) {
+  return *(const Raw<T, V>*)p;
 }
 
-__device__ __forceinline__ float load(const void* p, int type, long long i) {
-  return type == 1 ? widen(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+struct E4M3 {
+  uint8_t code;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void put(T* p, const float* v) {
+  if constexpr (std::is_same<T, E4M3>::value) {
+    if constexpr (V == 1) {
+      p->code = (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false) & 0xff);
+    } else {
+      int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+      a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
+      b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+      *(int2*)p = make_int2(a, b);
+    }
+  } else if constexpr (V == 1) {
+    narrow(v[0], p);
+  } else if constexpr (sizeof(T) == 4) {
+    *(f32x4*)p = (f32x4){v[0], v[1], v[2], v[3]};
+    *(f32x4*)(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, lapnys::bf16x2));
+    *(u32x4*)p = o;
+  }
 }
 
-__device__ __forceinline__ void store(void* p, int type, long long i, float v) {
-  if (type == 1)
-    narrow(v, (uint16_t*)p + i);
-  else
-    ((float*)p)[i] = v;
+template <typename T>
+__device__ __forceinline__ float rounded(float v) {
+  return sizeof(T) == 4 ? v : (float)(__bf16)v;
 }
 
-__device__ __forceinline__ float rounded(float v, int type) { return type == 1 ? (float)(__bf16)v : v; }
+struct Sum {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {  // keeps NaN
+  __device__ float operator()(float a, float b) const { return b > a || b != b ? b : a; }
+};
 
-// e4m3 code of v, |v| <= 448 (NaN gives NaN).
-__device__ __forceinline__ uint8_t e4m3(float v) {
-  return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+// Over the lanes of a row (TPR of them, or with TPR = 0 the whole workgroup), in an
+// order fixed by the lanes; every lane gets the results.  `shared` has N floats for
+// each wave; a call may use it again after another barrier.
+template <int TPR, int N, typename F>
+__device__ __forceinline__ void over_row(float (&v)[N], float* shared, F f) {
+#pragma unroll
+  for (int m = 1; m < (TPR ? TPR : 64); m *= 2)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = f(v[k], __shfl_xor(v[k], m));
+  if constexpr (TPR == 0) {
+    const int waves = blockDim.x / 64, wave = threadIdx.x / 64;
+    if (threadIdx.x % 64 == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) shared[wave * N + k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = shared[k];
+    for (int i = 1; i < waves; ++i)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = f(v[k], shared[i * N + k]);
+  }
 }
 
-__device__ __forceinline__ float stored_sum(const NormArgs& a, long long row, int c) {
-  const long long b = row / a.N, n = row % a.N;
-  float v = load(a.x, a.x_dtype, b * a.xs.b + (c / a.d) * a.xs.h + n * a.xs.n + c % a.d);
-  if (a.r) v += load(a.r, a.r_dtype, row * a.C + c);
-  return rounded(v, a.r_dtype);
-}
-
-// The largest |y| of a group is never below this when it makes a scale: its
+// The largest |y| that makes a scale is never below this: 448 times its
 // reciprocal stays finite.
 constexpr float kLeast = 0x1p-100f;
 
-__global__ __launch_bounds__(64) void forward_kernel(NormArgs a) {
-  const long long row = blockIdx.x;
-  const int lane = threadIdx.x;
-  float sum = 0.f;
-  for (int c = lane; c < a.C; c += 64) {
-    const float v = stored_sum(a, row, c);
-    sum += v * v;
+// Where a lane works: TPR lanes to a row, or with TPR = 0 the whole workgroup.
+template <int TPR>
+struct Place {
+  int lane, lanes, row, rows;  // of the row; rows side by side
+  __device__ Place() {
+    lanes = TPR ? TPR : blockDim.x;
+    lane = TPR ? threadIdx.x % TPR : threadIdx.x;
+    row = TPR ? threadIdx.x / TPR : 0;
+    rows = TPR ? kNarrow / TPR : 1;
   }
-  const float rstd = 1.f / sqrtf(wave_sum(sum) / (float)a.C + a.eps);
-  const int group = a.group ? a.group : a.C;
-  for (int g0 = 0; g0 < a.C; g0 += group) {
-    float scale = 1.f, inv = 1.f;
-    if (a.y_dtype == kE4M3) {
-      float top = 0.f;
-      for (int c = g0 + lane; c < g0 + group; c += 64) {
-        const float v = fabsf(stored_sum(a, row, c) * rstd * a.w[c]);
-        top = v > top || v != v ? v : top;
-      }
-      for (int m = 32; m; m >>= 1) {
-        const float o = __shfl_xor(top, m);
-        top = o > top || o != o ? o : top;
-      }
-      top = top < kLeast ? kLeast : top;
-      scale = top / 448.f;
-      inv = 448.f / top;
-      if (lane == 0) a.scale[(row * a.C + g0) / group] = scale;
+};
+
+// X, R, Y: types of x, r and s, and y.  CH chunks of V columns a lane.
+template <typename X, typename R, typename Y, int V, int TPR, int CH>
+__global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(NormArgs a) {
+  constexpr bool Q = std::is_same<Y, E4M3>::value;
+  __shared__ float shared[2][kWide / 64];
+  const Place<TPR> at;
+  const long long row = (long long)blockIdx.x * at.rows + at.row;
+  if (row >= a.rows) return;  // rows of part of a workgroup need no barrier
+  const uint32_t b = (uint32_t)row / (uint32_t)a.N, n = (uint32_t)row % (uint32_t)a.N;
+  const X* x = (const X*)a.x + b * a.xs.b + n * a.xs.n;
+  Raw<X, V> xr[CH];
+  Raw<R, V> rr[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * at.lanes + at.lane) * V;
+    if (c < a.C) {
+      const int h = c / a.d;
+      xr[k] = get<V>(x + h * a.xs.h + (c - h * a.d));
+      if (a.r) rr[k] = get<V>((const R*)a.r + row * a.C + c);
     }
-    for (int c = g0 + lane; c < g0 + group; c += 64) {
-      const float v = stored_sum(a, row, c), y = v * rstd * a.w[c];
-      if (a.s) store(a.s, a.r_dtype, row * a.C + c, v);
-      if (a.y_dtype == kE4M3)
-        ((uint8_t*)a.y)[row * a.C + c] = e4m3(y * inv);
-      else
-        store(a.y, a.y_dtype, row * a.C + c, y);
+  }
+  float v[CH][V], ss[1] = {0.f};
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const bool on = (k * at.lanes + at.lane) * V < a.C;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[k][i] = on ? rounded<R>(a.r ? xr[k][i] + rr[k][i] : xr[k][i]) : 0.f;
+      ss[0] += v[k][i] * v[k][i];
+    }
+  }
+  over_row<TPR>(ss, shared[0], Sum());
+  const float rstd = 1.f / sqrtf(ss[0] / (float)a.C + a.eps);
+  float top[1] = {0.f};
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * at.lanes + at.lane) * V;
+    if (c < a.C) {
+      if (a.s) put<R, V>((R*)a.s + row * a.C + c, v[k]);
+      const Raw<float, V> w = get<V>(a.w + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] *= rstd * w[i];
+      if constexpr (!Q) put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+    }
+    if constexpr (Q) {
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) t = Max()(t, fabsf(v[k][i]));
+      if (a.group) {
+        // A group lies in neighbouring lanes of one wave, within a chunk.
+        for (int m = 1; m < a.group / V; m *= 2) t = Max()(t, __shfl_xor(t, m));
+        t = t < kLeast ? kLeast : t;
+        if (c < a.C) {
+          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = t / 448.f;
+          const float inv = 448.f / t;
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[k][i] *= inv;
+          put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+        }
+      }
+      top[0] = Max()(top[0], t);
+    }
+  }
+  if constexpr (Q) {
+    if (a.group) return;
+    over_row<TPR>(top, shared[1], Max());
+    top[0] = top[0] < kLeast ? kLeast : top[0];
+    if (at.lane == 0) a.scale[row] = top[0] / 448.f;
+    const float inv = 448.f / top[0];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * at.lanes + at.lane) * V;
+      if (c >= a.C) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] *= inv;
+      put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
     }
   }
 }
 
-__global__ __launch_bounds__(64) void backward_kernel(NormArgs a) {
-  const int lane = threadIdx.x;
-  const long long per = (a.rows + a.parts - 1) / a.parts;
-  const long long r0 = blockIdx.x * per, r1 = min(a.rows, r0 + per);
-  if (a.dw)
-    for (int c = lane; c < a.C; c += 64) a.part[(long long)blockIdx.x * a.C + c] = 0.f;
-  for (long long row = r0; row < r1; ++row) {
-    const long long o = row * a.C;
-    float ss = 0.f, dot = 0.f;
-    for (int c = lane; c < a.C; c += 64) {
-      const float v = load(a.s, a.r_dtype, o + c);
-      ss += v * v;
-      dot += load(a.dy, a.y_dtype, o + c) * a.w[c] * v;
+template <typename X, typename R, typename Y, int V, int TPR, int CH>
+__global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(NormArgs a) {
+  __shared__ float shared[2][2 * kWide / 64];
+  const Place<TPR> at;
+  const long long step = (long long)gridDim.x * at.rows;
+  Raw<float, V> w[CH];
+  float dw[CH][V];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * at.lanes + at.lane) * V;
+    if (c < a.C) w[k] = get<V>(a.w + c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[k][i] = 0.f;
+  }
+  struct Row {
+    Raw<R, V> s[CH], ds[CH];
+    Raw<Y, V> dy[CH];
+  };
+  auto load = [&](long long row, Row& r) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * at.lanes + at.lane) * V;
+      if (row < a.rows && c < a.C) {
+        r.s[k] = get<V>((const R*)a.s + row * a.C + c);
+        r.dy[k] = get<V>((const Y*)a.dy + row * a.C + c);
+        if (a.ds) r.ds[k] = get<V>((const R*)a.ds + row * a.C + c);
+      }
     }
-    const float rstd = 1.f / sqrtf(wave_sum(ss) / (float)a.C + a.eps);
-    const float mean = wave_sum(dot) * rstd / (float)a.C;
-    const long long b = row / a.N, n = row % a.N;
-    for (int c = lane; c < a.C; c += 64) {
-      const float u = load(a.s, a.r_dtype, o + c) * rstd, dy = load(a.dy, a.y_dtype, o + c);
-      const float v = rstd * (dy * a.w[c] - u * mean) + (a.ds ? load(a.ds, a.r_dtype, o + c) : 0.f);
-      if (a.dr) store(a.dr, a.r_dtype, o + c, v);
-      if (a.dx) store(a.dx, a.x_dtype, b * a.xs.b + (c / a.d) * a.xs.h + n * a.xs.n + c % a.d, v);
-      if (a.dw) a.part[(long long)blockIdx.x * a.C + c] += dy * u;
+  };
+  // The next row's loads are under way during a row where registers allow.
+  constexpr bool AHEAD = V * CH <= 8;
+  Row next;
+  long long row = (long long)blockIdx.x * at.rows + at.row;
+  if (AHEAD) load(row, next);
+  // Every lane makes the same number of turns: the whole workgroup meets in over_row.
+  for (int turn = 0; row - at.row < a.rows; row += step, turn ^= 1) {
+    if (!AHEAD) load(row, next);
+    const Row r = next;
+    if (AHEAD) load(row + step, next);
+    const bool on = row < a.rows;
+    float sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      if (on && (k * at.lanes + at.lane) * V < a.C)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          sums[0] += r.s[k][i] * r.s[k][i];
+          sums[1] += r.dy[k][i] * w[k][i] * r.s[k][i];
+        }
+    // Two slots in turn: a wave may still read one while another is a row further.
+    over_row<TPR>(sums, shared[turn], Sum());
+    const float rstd = 1.f / sqrtf(sums[0] / (float)a.C + a.eps);
+    const float mean = sums[1] * rstd / (float)a.C;
+    if (!on) continue;
+    const uint32_t b = (uint32_t)row / (uint32_t)a.N, n = (uint32_t)row % (uint32_t)a.N;
+    X* dx = (X*)a.dx + b * a.xs.b + n * a.xs.n;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * at.lanes + at.lane) * V;
+      if (c >= a.C) continue;
+      float g[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float u = r.s[k][i] * rstd;
+        dw[k][i] += r.dy[k][i] * u;
+        g[i] = rstd * (r.dy[k][i] * w[k][i] - u * mean) + (a.ds ? r.ds[k][i] : 0.f);
+      }
+      if (a.dr) put<R, V>((R*)a.dr + row * a.C + c, g);
+      if (a.dx) {
+        const int h = c / a.d;
+        put<X, V>(dx + h * a.xs.h + (c - h * a.d), g);
+      }
     }
+  }
+  if (!a.dw) return;
+  // Rows that a workgroup takes side by side have a part each.
+  float* part = a.part + ((long long)blockIdx.x * at.rows + at.row) * a.C;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * at.lanes + at.lane) * V;
+    if (c < a.C)
+#pragma unroll
+      for (int i = 0; i < V; ++i) part[c + i] = dw[k][i];
   }
 }
 
-__global__ __launch_bounds__(64) void weight_kernel(NormArgs a) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= a.C) return;
+// Adds the parts of dw: a workgroup takes 64 columns, its waves every 4th part each.
+__global__ __launch_bounds__(kNarrow) void norm_weight_kernel(NormArgs a) {
+  constexpr int WAVES = kNarrow / 64;
+  __shared__ float sums[WAVES][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int c = blockIdx.x * 64 + lane;
   float sum = 0.f;
-  for (int i = 0; i < a.parts; ++i) sum += a.part[(long long)i * a.C + c];
+  if (c < a.C)
+    for (int i = wave; i < a.parts; i += WAVES) sum += a.part[(long long)i * a.C + c];
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave || c >= a.C) return;
+  for (int i = 1; i < WAVES; ++i) sum += sums[i][lane];
   a.dw[c] = sum;
+}
+
+// How rows of C columns are laid on lanes: TPR lanes of a workgroup of kNarrow, or
+// (tpr = 0) a workgroup of `block` lanes.
+struct Shape {
+  int v, tpr, ch, block;
+  int rows() const { return tpr ? kNarrow / tpr : 1; }
+};
+
+Shape shape_of(int C, bool vec) {
+  const int v = vec ? 8 : 1, chunks = (C + v - 1) / v;
+  auto wide = [&](int ch) { return Shape{v, 0, ch, ((chunks + ch - 1) / ch + 63) / 64 * 64}; };
+  if (vec) {
+    if (chunks <= 16) return {v, 16, 1, kNarrow};
+    if (chunks <= 64) return {v, 64, 1, kNarrow};
+    return wide(chunks <= 512 ? 1 : 2);
+  }
+  if (chunks <= 64) return {v, 64, 1, kNarrow};
+  return wide(chunks <= 4096 ? 4 : 16);
+}
+
+template <typename F>
+void with_shape(const Shape& s, F f) {
+  if (s.v == 8) {
+    if (s.tpr == 16) return f(Int<8>(), Int<16>(), Int<1>());
+    if (s.tpr == 64) return f(Int<8>(), Int<64>(), Int<1>());
+    return s.ch == 1 ? f(Int<8>(), Int<0>(), Int<1>()) : f(Int<8>(), Int<0>(), Int<2>());
+  }
+  if (s.tpr == 64) return f(Int<1>(), Int<64>(), Int<1>());
+  return s.ch == 4 ? f(Int<1>(), Int<0>(), Int<4>()) : f(Int<1>(), Int<0>(), Int<16>());
+}
+
+template <typename F>
+void with_types(const NormArgs& a, F f) {
+  auto y = [&](auto x, auto r) {
+    if (a.y_dtype == 2) return f(x, r, E4M3());
+    if (a.y_dtype == 1) return f(x, r, uint16_t());
+    return f(x, r, float());
+  };
+  auto r = [&](auto x) { a.r_dtype == 1 ? y(x, uint16_t()) : y(x, float()); };
+  a.x_dtype == 1 ? r(uint16_t()) : r(float());
 }
 
 }  // namespace
 
-int norm_parts(long long rows, int) { return (int)(rows < 512 ? rows : 512); }
+// Enough workgroups to fill the chip, and rows enough for each that the parts of
+// dw are small beside the rows.
+static int norm_groups(long long rows, const Shape& shape) {
+  const long long n = (rows + shape.rows() - 1) / shape.rows();
+  return (int)(n < 1024 ? n : 1024);
+}
+
+size_t norm_part_count(const NormArgs& a) {
+  size_t most = 0;
+  for (bool vec : {false, true}) {
+    const Shape shape = shape_of(a.C, vec);
+    const size_t n = (size_t)norm_groups(a.rows, shape) * shape.rows();
+    most = n > most ? n : most;
+  }
+  return most;
+}
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
-  forward_kernel<<<dim3((unsigned)a.rows), dim3(64), 0, s>>>(a);
+  const Shape shape = shape_of(a.C, a.vec);
+  const dim3 grid((unsigned)((a.rows + shape.rows() - 1) / shape.rows())), block(shape.block);
+  with_types(a, [&](auto x, auto r, auto y) {
+    with_shape(shape, [&](auto v, auto tpr, auto ch) {
+      norm_forward_kernel<decltype(x), decltype(r), decltype(y), decltype(v)::value, decltype(tpr)::value,
+                          decltype(ch)::value><<<grid, block, 0, s>>>(a);
+    });
+  });
   return hipGetLastError();
 }
 
-hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
-  backward_kernel<<<dim3((unsigned)a.parts), dim3(64), 0, s>>>(a);
+hipError_t launch_norm_backward(const NormArgs& args, hipStream_t s) {
+  NormArgs a = args;
+  const Shape shape = shape_of(a.C, a.vec);
+  const int groups = norm_groups(a.rows, shape);
+  a.parts = groups * shape.rows();
+  with_types(a, [&](auto x, auto r, auto y) {
+    if constexpr (!std::is_same<decltype(y), E4M3>::value)
+      with_shape(shape, [&](auto v, auto tpr, auto ch) {
+        norm_backward_kernel<decltype(x), decltype(r), decltype(y), decltype(v)::value, decltype(tpr)::value,
+                             decltype(ch)::value><<<dim3(groups), dim3(shape.block), 0, s>>>(a);
+      });
+  });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
-  weight_kernel<<<dim3((unsigned)((a.C + 63) / 64)), dim3(64), 0, s>>>(a);
+  norm_weight_kernel<<<dim3((unsigned)((a.C + 63) / 64)), dim3(kNarrow), 0, s>>>(a);
   return hipGetLastError();
 }
 
