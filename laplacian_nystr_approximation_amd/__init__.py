@@ -28,8 +28,9 @@ _MIX_NAMES = {
 
 
 def __getattr__(name):
-    if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".lapnys", __name__), name)
-    if name in _MIX_NAMES:
-        return getattr(importlib.import_module(".lapmix", __name__), name)
-    raise AttributeError(name)
+    module = ".lapnys" if name in _BINDING_NAMES else ".lapmix" if name in _MIX_NAMES else None
+    if module is None:
+        raise AttributeError(name)
+    # Kept in the module's namespace: later uses find it without coming here.
+    value = globals()[name] = getattr(importlib.import_module(module, __name__), name)
+    return value

@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from .lapnys import LAPNYS_BF16, LAPNYS_F32, _check, _lib, _ptr, _stream, _ws
+from .lapnys import LAPNYS_BF16, LAPNYS_F32, _check, _lib, _stream as _given_stream, _ws
 
 LAPMIX_E4M3 = 2
 LAPMIX_GATE_LOG = 1
@@ -85,6 +85,22 @@ def make_norm_params(*, B, H, N, d, x_dtype="f32", r_dtype="f32", y_dtype="f32",
                               _NAMES.get(y_dtype, y_dtype), group, eps, 0)
 
 
+# Decoding steps are a few microseconds long on the GPU, so these checks go by the
+# shortest ways to a tensor's facts.
+def _stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _given_stream(stream)
+
+
+def _device_ptr(t):
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be device tensors (got a tensor on the host)")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
 def _flat(name, t, size, count):
     """Pointer of a dense tensor argument that holds at least ``count`` elements of ``size`` bytes."""
     if t is None or isinstance(t, int):
@@ -92,28 +108,28 @@ def _flat(name, t, size, count):
     if t.element_size() != size or t.numel() < count:
         raise ValueError(f"{name}: expected at least {count} elements of {size} bytes, "
                          f"got {t.numel()} of {t.element_size()}")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return _device_ptr(t)
 
 
 def _heads(name, t, size, p):
     """(pointer, strides) of a [B, H, N, d] tensor argument; strides None for a raw pointer."""
-    if isinstance(t, int) or t is None:
+    if t is None or isinstance(t, int):
         return t, None
-    if t.element_size() != size or t.shape != (p.B, p.H, p.N, p.d):
-        raise ValueError(f"{name}: expected [{p.B}, {p.H}, {p.N}, {p.d}] of {size} bytes, "
+    B, H, N, d = p.B, p.H, p.N, p.d
+    if t.element_size() != size or t.shape != (B, H, N, d):
+        raise ValueError(f"{name}: expected [{B}, {H}, {N}, {d}] of {size} bytes, "
                          f"got {list(t.shape)} of {t.element_size()}")
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be device tensors (got a tensor on the host)")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    ptr = _device_ptr(t)
     b, h, n, c = t.stride()
-    if c != 1 and p.d != 1:
+    if c != 1 and d != 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {c})")
     # Strides of dimensions of size 1 do not matter; all zero would mean a dense tensor.
-    st = (b if p.B > 1 else 0, h if p.H > 1 else 0, n if p.N > 1 else 0)
-    if not any(st) and p.B * p.H * p.N > 1:
+    st = (b if B > 1 else 0, h if H > 1 else 0, n if N > 1 else 0)
+    if not (b or h or n) and B * H * N > 1:
         raise ValueError(f"{name}: one row repeated for every token is not supported")
-    return t.data_ptr(), st
+    return ptr, st
 
 
 def _agree(name, st, other, of):
