@@ -36,9 +36,9 @@
  * output need no copy; strides of all zero mean dense C order.  Strides are
  * at least 0; elements of a tensor that is written may not coincide, inputs
  * may repeat (stride 0).  r, s, y, dy, ds and dr of the norm are dense
- * [B, N, C].  Base addresses need the alignment of an element; where bases
- * and strides are multiples of 16 bytes (and d of 16 bytes' elements) the
- * kernels move 16 bytes a lane.
+ * [B, N, C].  Base addresses need the alignment of an element; the kernels are
+ * fastest where d and the strides are multiples of 4 elements (for the norm of
+ * 8) and bases of 16 bytes.
  *
  * Precision: inputs widen exactly to float32; gates, states, products, norms
  * and their sums are float32; each output is rounded once, to nearest even.
@@ -67,7 +67,7 @@ enum { LAPMIX_GATE_LOG = 1u, LAPMIX_COUPLED = 2u };
 
 /* The forward can keep the state before every LAPMIX_SCAN_TILE-th token for
  * the backward pass. */
-#define LAPMIX_SCAN_TILE 256
+#define LAPMIX_SCAN_TILE 128
 
 typedef struct {
   int32_t B, H, N, d;   /* batches, heads, tokens, channels */
@@ -136,8 +136,8 @@ int lapmix_scan_step(const void* x, const void* g, const int32_t* slots, const f
  * of r_dtype, or NULL if it is not needed; it may be r itself.  y: [B, N, C].
  * scale: float32 [B, N, C / group] for LAPMIX_E4M3, else NULL.  A group whose
  * largest |y| lies below 2^-100 takes the scale 2^-100 / 448.  A group
- * narrower than the row needs d and x_stride to be multiples of 8 elements and
- * bases of 16 bytes (LAPNYS_ERR_UNSUPPORTED).  Rows have up to 16384 columns
+ * narrower than the row needs d and x_stride to be multiples of 8 elements, and
+ * bases of 16 bytes (y: 8), else LAPNYS_ERR_UNSUPPORTED.  Rows have up to 16384 columns
  * (wider ones: LAPNYS_ERR_UNSUPPORTED). */
 int lapmix_norm_forward(const void* x, const void* r, const float* w, void* s, void* y, float* scale,
                         const lapmix_norm_params* p, hipStream_t stream);

@@ -117,11 +117,11 @@ bool take_strides(const int64_t in[3], int32_t B, int32_t H, int32_t N, int32_t 
 
 bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
-// Bases and the strides of dimensions that are stepped along allow 16-byte accesses.
-bool vec_view(const View& v) {
-  if (v.base & 15) return false;
-  const int64_t per = 16 / v.esize;
-  if (v.width % per) return false;
+// Width and the strides of dimensions that are stepped along are multiples of `per`
+// elements, and the base of as many, or of 16 bytes.
+bool vec_view(const View& v, int64_t per) {
+  const uintptr_t bytes = (uintptr_t)(per * v.esize);
+  if (v.base % (bytes < 16 ? bytes : 16) || v.width % per) return false;
   for (int i = 0; i < v.nd; ++i)
     if (v.s[i] % per) return false;
   return true;
@@ -184,7 +184,7 @@ int scan_forward(const void* x, const void* g, const float* h0, const int32_t* l
     return LAPNYS_ERR_INVALID_ARG;
   st = check_workspace(ws, ws_bytes, need);
   if (st != LAPNYS_OK) return st;
-  a.vec = vec_view(vx) && vec_view(vg) && vec_view(vy);
+  a.vec = vec_view(vx, 4) && vec_view(vg, 4) && vec_view(vy, 4);
   a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.y = y, a.hN = hN, a.states = states;
   (void)hipGetLastError();
   return ok(lapmix::launch_scan_forward(a, ws, s), "recurrence launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;
@@ -215,7 +215,7 @@ int scan_backward(const void* x, const void* g, const float* states, const int32
     return LAPNYS_ERR_INVALID_ARG;
   st = check_workspace(ws, ws_bytes, need);
   if (st != LAPNYS_OK) return st;
-  a.vec = vec_view(vx) && vec_view(vg) && vec_view(vdy) && vec_view(vdx) && vec_view(vdg);
+  a.vec = vec_view(vx, 4) && vec_view(vg, 4) && vec_view(vdy, 4) && vec_view(vdx, 4) && vec_view(vdg, 4);
   a.x = x, a.g = g, a.states = const_cast<float*>(states), a.lengths = lengths;
   a.dy = dy, a.dhN = dhN, a.dx = dx, a.dg = dg, a.dh0 = dh0;
   (void)hipGetLastError();
@@ -244,7 +244,7 @@ int scan_step(const void* x, const void* g, const int32_t* slots, const float* h
   lapmix::StepArgs t = {};
   t.B = a.B, t.H = a.H, t.d = a.d, t.n_slots = n_slots;
   t.log_gate = a.log_gate, t.coupled = a.coupled, t.dtype = a.dtype;
-  t.vec = vec_view(vx) && vec_view(vg) && vec_view(vy) && aligned(h_in, 16) && aligned(h_out, 16);
+  t.vec = vec_view(vx, 4) && vec_view(vg, 4) && vec_view(vy, 4) && aligned(h_in, 16) && aligned(h_out, 16);
   t.xs = a.xs, t.gs = a.gs, t.ys = a.ys;
   t.x = x, t.g = g, t.slots = slots, t.h_in = h_in, t.h_out = h_out, t.y = y;
   (void)hipGetLastError();
@@ -297,9 +297,9 @@ int norm_forward(const void* x, const void* r, const float* w, void* s, void* y,
   const View out[] = {vs, vy, vsc};
   const View in[] = {vx, vw, r == s ? dense_view(nullptr, 0, 4) : vr};
   if (!outputs_apart(out, 3, in, 3)) return LAPNYS_ERR_INVALID_ARG;
-  // Lanes hold 8 neighbouring columns: 16 bytes of bf16 and two times 16 of float32.
-  a.vec = vec_view(vx) && a.d % 8 == 0 && aligned(r, 16) && aligned(w, 16) && aligned(s, 16) &&
-          aligned(y, e4m3 ? 8 : 16) && (a.xs.b | a.xs.h | a.xs.n) % 8 == 0;
+  // Lanes hold 8 neighbouring columns: 16 bytes of bf16 or 32 of float32.
+  a.vec = vec_view(vx, 8) && aligned(r, 16) && aligned(w, 16) && aligned(s, 16) &&
+          aligned(y, e4m3 ? 8 : 16);
   if (a.group && !a.vec) return LAPNYS_ERR_UNSUPPORTED;
   a.x = x, a.r = r, a.w = w, a.s = s, a.y = y, a.scale = scale;
   (void)hipGetLastError();
@@ -340,7 +340,7 @@ int norm_backward(const void* dy, const void* s, const float* w, const void* ds,
   st = check_workspace(ws, ws_bytes, need);
   if (st != LAPNYS_OK) return st;
   a.vec = a.d % 8 == 0 && aligned(dy, 16) && aligned(s, 16) && aligned(w, 16) && aligned(ds, 16) && aligned(dr, 16) &&
-          (!dx || (vec_view(vdx) && (a.xs.b | a.xs.h | a.xs.n) % 8 == 0));
+          (!dx || vec_view(vdx, 8));
   a.dy = dy, a.s = const_cast<void*>(s), a.w = w, a.ds = ds, a.dr = dr, a.dx = dx, a.dw = dw, a.part = (float*)ws;
   (void)hipGetLastError();
   return ok(lapmix::launch_norm_backward(a, stream), "norm backward launch") ? LAPNYS_OK : LAPNYS_ERR_HIP;

@@ -9,9 +9,10 @@ namespace lapmix {
 using lapnys::f32x2;
 using lapnys::f32x4;
 using lapnys::u32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 using lapnys::widen;
 
-constexpr int kTile = 256;  // tokens of a tile (LAPMIX_SCAN_TILE)
+constexpr int kTile = 128;  // tokens of a tile (LAPMIX_SCAN_TILE)
 
 // Element strides of a [B, H, N, d] tensor whose channels are contiguous.
 struct Strides {

@@ -4,23 +4,25 @@
 // h -> A h + S (A the product of its gates, S its result from a zero state),
 // and two runs compose to (A2 A1, A2 S1 + S2).  A workgroup takes a tile of
 // kTile tokens by a few dozen columns (batch, head, channel): each lane holds a
-// few consecutive tokens of 16 bytes' worth of neighbouring channels, walks them
-// once for its (A, S), the lanes' pairs are composed over the wave by lane
-// exchange and over the workgroup through LDS, and with the state before the tile
-// known each lane walks its tokens a second time, in registers, and writes y.
-// x and g are read once and y is written once: the kernel is bound by HBM.
+// few consecutive tokens of V neighbouring channels, walks them once for its
+// (A, S), the lanes' pairs are composed over the wave by lane exchange and over
+// the workgroup through LDS, and with the state before the tile known each lane
+// walks its tokens a second time, in registers, and writes y.  x and g are read
+// once and y is written once: the kernel is bound by HBM.  While a workgroup
+// works on a tile, the loads of its next one are under way.
 //
 // The state before a tile comes from one of two places.
-//  - Loop form: the workgroup takes all tiles of its columns one after the other.
-//  - Chain form, for few columns: every tile is a workgroup of its own.  Tiles
-//    publish their (A, S), and every 16th tile the pair of its 16 tiles and every
-//    256th that of its 256, so that a tile composes at most 15 + 15 pairs and
-//    one for each 65536 tokens before it.  Which pairs are composed, and in which
+//  - Loop form: a workgroup takes all tiles of its columns one after the other.
+//  - Chain form, for few columns: several workgroups share the tiles of a group of
+//    columns and take them as they come.  A tile publishes its (A, S), every kFan-th tile also the pair of the last kFan tiles,
+//    every kFan^2-th that of the last kFan^2, and so on, so that a tile composes at
+//    most kFan - 1 pairs of each level.  Which pairs are composed, and in which
 //    order, depends on the tile's place alone: results repeat bit for bit.
 //
-// Waits end: a tile takes its place from a counter, in the order in which
-// workgroups start, so it waits only for tiles of workgroups that have started
-// before it, and the first unfinished one of those waits for nothing.
+// Waits end: workgroups draw a group's tiles from the group's counter, in order, and
+// finish one before they draw the next, so the lowest unfinished tile is being
+// worked on and waits only for tiles below it, which are finished.  (A counter
+// for each group: one for all of them is a bottleneck, about 15 ns a draw.)
 //
 // The backward pass runs the tiles from the last to the first with r = f dh in
 // the place of h (r_t = f_t (dy_t + r_{t+1})), and recomputes the tile's h from
@@ -33,7 +35,10 @@ namespace lapmix {
 
 namespace {
 
-constexpr int kFan = 16;  // tiles whose pairs are composed into one
+constexpr int kFan = 8;      // pairs of a level that make one of the next
+constexpr int kLevels = 5;   // the highest level's pairs stand for kFan^4 tiles
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 
 struct Pair {
   float a, s;
@@ -45,12 +50,13 @@ __device__ __forceinline__ Pair compose(Pair first, Pair then) { return {then.a 
 // published A is never that pattern (a NaN is stored as the canonical one), so
 // the 64-bit word tells by itself whether it is there, and no fence is needed.
 constexpr uint64_t kUnset = ~(uint64_t)0;
-constexpr int kFillThreads = 256;
 
-__global__ __launch_bounds__(kFillThreads) void scan_fill_kernel(uint64_t* words, long long n) {
-  const long long i = (long long)blockIdx.x * kFillThreads + threadIdx.x;
-  // Word 0 is the tile counter.
-  if (i < n) words[i] = i == 0 ? 0 : kUnset;
+// Words of a counter: each has 256 bytes of its own.
+constexpr int kCounter = 32;
+
+__global__ __launch_bounds__(kThreads) void scan_fill_kernel(uint64_t* words, long long counters, long long n) {
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i < n) words[i] = i < counters ? 0 : kUnset;
 }
 
 __device__ __forceinline__ void publish(uint64_t* at, Pair p) {
@@ -80,16 +86,16 @@ __device__ __forceinline__ Pair wait_for(const uint64_t* at, uint64_t w) {
   return pair_of(w);
 }
 
-// The words of a launch's chain: the counter, then for each level [places][columns].
+// The words of a launch's chain: the groups' counters, then for each level [places][columns].
 struct Chain {
   uint64_t* words;
   long long columns;
-  long long level[3];  // first word of each level
+  long long level[kLevels];  // first word of each level
 };
 
-__host__ __device__ inline long long chain_layout(int ntiles, long long columns, long long level[3]) {
-  long long at = 32, n = ntiles;  // the counter has 256 bytes of its own
-  for (int i = 0; i < 3; ++i) {
+long long chain_layout(int ntiles, long long columns, long long groups, long long level[kLevels]) {
+  long long at = groups * kCounter, n = ntiles;
+  for (int i = 0; i < kLevels; ++i) {
     level[i] = at;
     at += n * columns;
     n /= kFan;
@@ -97,73 +103,51 @@ __host__ __device__ inline long long chain_layout(int ntiles, long long columns,
   return at;
 }
 
-// The pair of everything before place p for the columns of a workgroup of NT lanes,
-// returned to the lanes tid < WIDTH, each with its own column's `own` pair.  The
-// pairs to compose are spread over the workgroup (SLOTS lanes a column), so all
-// of them are in flight at once.  All lanes call it.
-template <int NT, int WIDTH>
-__device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, uint32_t base, Pair own) {
-  constexpr int SLOTS = NT / WIDTH < kFan ? NT / WIDTH : kFan, EACH = kFan / SLOTS;
-  __shared__ Pair part[2][SLOTS][WIDTH];
-  const int tid = threadIdx.x, slot = tid / WIDTH, lane = tid % WIDTH;
-  const bool on = base + lane < (uint64_t)c.columns;
-  uint64_t* w = c.words + (on ? base + lane : 0);
-  const int p0 = p % kFan, q = p / kFan, q0 = q % kFan, t = q / kFan;
-  if (slot == 0 && on && p < last) publish(w + c.level[0] + (long long)p * c.columns, own);
-  const uint64_t* near = w + c.level[0] + (long long)(p - p0) * c.columns;
-  const uint64_t* mid = w + c.level[1] + (long long)(q - q0) * c.columns;
-  uint64_t wn[EACH], wm[EACH];
-  const bool works = on && slot < SLOTS;
+// Publishes the pair `own` of place p in one column and returns the pair of
+// everything before it.  The first levels' pairs are asked for together.
+__device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, uint32_t col, Pair own) {
+  constexpr int FIRST = 2;
+  uint64_t* const w = c.words + col;
+  if (p < last) publish(w + c.level[0] + (long long)p * c.columns, own);
+  uint64_t seen[FIRST][kFan - 1];
+  int q = p;
 #pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    const int k = slot * EACH + i;
-    wn[i] = works && k < p0 ? peek(near + k * c.columns) : 0;
-    wm[i] = works && k < q0 ? peek(mid + k * c.columns) : 0;
+  for (int l = 0; l < FIRST; ++l, q /= kFan) {
+    const uint64_t* at = w + c.level[l] + (long long)(q - q % kFan) * c.columns;
+#pragma unroll
+    for (int i = 0; i < kFan - 1; ++i) seen[l][i] = i < q % kFan ? peek(at + i * c.columns) : 0;
   }
-  Pair sum = {1.f, 0.f};
+  Pair before = {1.f, 0.f};
+  bool full = true;  // the levels so far end with this place
+  q = p;
 #pragma unroll
-  for (int i = 0; i < EACH; ++i)
-    if (works && slot * EACH + i < p0) sum = compose(sum, wait_for(near + (slot * EACH + i) * c.columns, wn[i]));
-  if (slot < SLOTS) part[0][slot][lane] = sum;
-  __syncthreads();
-  Pair before = {1.f, 0.f}, sixteen = {1.f, 0.f};
-  if (slot == 0) {
+  for (int l = 0; l < kLevels; ++l, q /= kFan) {
+    const bool top = l == kLevels - 1;
+    const int n = top ? q : q % kFan;
+    const uint64_t* at = w + c.level[l] + (long long)(q - n) * c.columns;
+    Pair sum = {1.f, 0.f};
+    if (l < FIRST) {
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) before = compose(before, part[0][i][lane]);
-    // Published before anything else is waited for: the next tiles need it.
-    if (p0 == kFan - 1) {
-      sixteen = compose(before, own);
-      if (on && p < last) publish(w + c.level[1] + (long long)q * c.columns, sixteen);
+      for (int i = 0; i < kFan - 1; ++i)
+        if (i < n) sum = compose(sum, wait_for(at + i * c.columns, seen[l][i]));
+    } else {
+      for (int i0 = 0; i0 < n; i0 += kFan) {
+        uint64_t v[kFan];
+#pragma unroll
+        for (int i = 0; i < kFan; ++i) v[i] = i0 + i < n ? peek(at + (i0 + i) * c.columns) : 0;
+#pragma unroll
+        for (int i = 0; i < kFan; ++i)
+          if (i0 + i < n) sum = compose(sum, wait_for(at + (i0 + i) * c.columns, v[i]));
+      }
     }
-  }
-  if (q == 0) return before;
-  sum = {1.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < EACH; ++i)
-    if (works && slot * EACH + i < q0) sum = compose(sum, wait_for(mid + (slot * EACH + i) * c.columns, wm[i]));
-  if (slot < SLOTS) part[1][slot][lane] = sum;
-  __syncthreads();
-  if (slot == 0) {
-    Pair m = {1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) m = compose(m, part[1][i][lane]);
-    if (p0 == kFan - 1 && q0 == kFan - 1 && on && p < last)
-      publish(w + c.level[2] + (long long)t * c.columns, compose(m, sixteen));
-    before = compose(m, before);
-  }
-  if (t == 0) return before;
-  sum = {1.f, 0.f};
-  const uint64_t* far = w + c.level[2];
-  const int each = (t + SLOTS - 1) / SLOTS;
-  for (int k = slot * each; works && k < min(t, slot * each + each); ++k)
-    sum = compose(sum, wait_for(far + k * c.columns, peek(far + k * c.columns)));
-  if (slot < SLOTS) part[0][slot][lane] = sum;
-  __syncthreads();
-  if (slot == 0) {
-    Pair m = {1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) m = compose(m, part[0][i][lane]);
-    before = compose(m, before);
+    // The next level's pair goes out before that level is waited for.
+    full = full && !top && n == kFan - 1;
+    if (full) {
+      own = compose(sum, own);
+      if (p < last) publish(w + c.level[l + 1] + (long long)(q / kFan) * c.columns, own);
+    }
+    before = compose(sum, before);
+    if (q < kFan) break;
   }
   return before;
 }
@@ -185,72 +169,58 @@ __device__ __forceinline__ void gate(float g, float& f, float& rest) {
   }
 }
 
-// A gate in one register, for a gate that is needed with both f and 1 - f again
-// later: the smaller of them, with the sign bit where it is f.
-__device__ __forceinline__ float pack_gate(float f, float rest) {
-  return f < rest ? -f : fabsf(rest);
-}
-
-__device__ __forceinline__ void unpack_gate(float c, float& f, float& rest) {
-  const float small = fabsf(c), big = 1.f - small;
-  const bool is_f = __float_as_uint(c) >> 31;
-  f = is_f ? small : big;
-  rest = is_f ? big : small;
-}
-
-// Keeps a value in its register: what is derived from it again later is derived
-// again, and does not stay alive in between.
-__device__ __forceinline__ void keep(float& v) { asm volatile("" : "+v"(v)); }
-
-// V neighbouring channels of a token, as loaded: 16 bytes, or one element.
+// V neighbouring channels of a token, as loaded.
 template <typename T, int V>
-struct Raw {
-  using type = u32x4;
-};
+struct Raw;
 template <typename T>
 struct Raw<T, 1> {
-  using type = T;
+  T e;
+  __device__ __forceinline__ float operator[](int) const { return widen(e); }
+};
+template <>
+struct Raw<float, 4> {
+  f32x4 e;
+  __device__ __forceinline__ float operator[](int v) const { return e[v]; }
+};
+template <>
+struct Raw<uint16_t, 4> {
+  u32x2 e;
+  __device__ __forceinline__ float operator[](int v) const {
+    return __uint_as_float(v % 2 ? e[v / 2] & 0xffff0000u : e[v / 2] << 16);
+  }
 };
 
-template <typename T, int V>
-__device__ __forceinline__ float element(const typename Raw<T, V>::type& raw, int v) {
-  if constexpr (V == 1)
-    return widen(raw);
-  else if constexpr (sizeof(T) == 4)
-    return __uint_as_float(raw[v]);
-  else
-    return __uint_as_float(v % 2 ? raw[v / 2] & 0xffff0000u : raw[v / 2] << 16);
-}
-
-template <typename T, int V>
+template <int V, typename T>
 __device__ __forceinline__ void put(T* at, const float* v) {
   if constexpr (V == 1) {
     narrow(v[0], at);
   } else if constexpr (sizeof(T) == 4) {
     *(f32x4*)at = (f32x4){v[0], v[1], v[2], v[3]};
   } else {
-    u32x4 out;
+    u32x2 out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       out[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, lapnys::bf16x2));
-    *(u32x4*)at = out;
+    *(u32x2*)at = out;
   }
 }
 
-// Geometry of a workgroup of NT lanes with L tokens and V channels a lane.
-template <int NT, int L, int V>
-struct Tile {
-  static constexpr int kCols = NT * L / kTile;  // lanes side by side
-  static constexpr int kWidth = kCols * V;      // columns
-  static constexpr int kWaves = NT / 64;
-  static_assert(kCols >= 1 && kCols <= 32 && kWidth <= 64, "a wave holds whole rows of lanes");
+// A lane's share of a tile: L tokens of V channels; COLS lanes side by side span
+// 128 bytes of a token (64 bytes or more in the form for unaligned tensors).
+template <typename T, bool VEC>
+struct Geometry {
+  static constexpr int V = VEC ? 4 : 1;
+  static constexpr int COLS = VEC ? 32 / sizeof(T) : 32;
+  static constexpr int L = kTile * COLS / kThreads;
+  static constexpr int WIDTH = COLS * V;  // columns of a workgroup
+  static_assert(WIDTH >= 32 && WIDTH <= 64 && 64 % COLS == 0, "one wave looks after the columns' states");
 };
 
-// Exclusive scan of the lanes' pairs over the tile's rows, in the order of rising
-// tokens (or falling ones).  Returns the pair of the rows before the lane's within
-// its wave; `total` receives the waves' pairs.
+// Composes the lanes' pairs over the wave's rows in the order of rising tokens (or
+// falling ones).  p becomes the pair up to and with the lane's row, `before` that
+// of the rows before it.
 template <int COLS, int V, bool REVERSE>
-__device__ __forceinline__ void wave_scan(Pair p[V], Pair before[V]) {
+__device__ __forceinline__ void wave_scan(Pair (&p)[V], Pair (&before)[V]) {
   const int lane = threadIdx.x & 63;
   const int row = REVERSE ? (63 - lane) / COLS : lane / COLS;
   auto other = [&](float v, int rows) {
@@ -272,18 +242,17 @@ __device__ __forceinline__ void wave_scan(Pair p[V], Pair before[V]) {
 
 // What a lane is in charge of.
 struct Lane {
-  uint32_t col;  // first column
-  bool on;       // columns exist
+  bool on;       // its columns exist
   int len;       // tokens of the sequence
-  int64_t x, g, y;
+  int64_t x, g, y;  // offsets of token 0
 };
 
 __device__ __forceinline__ Lane lane_of(const ScanArgs& a, uint32_t col) {
   Lane l;
   l.on = col < (uint32_t)a.columns;
-  l.col = l.on ? col : 0;
-  const uint32_t c = l.col % (uint32_t)a.d, bh = l.col / (uint32_t)a.d;
-  const uint32_t h = bh % (uint32_t)a.H, b = bh / (uint32_t)a.H;
+  if (!l.on) col = 0;
+  const uint32_t bh = col / (uint32_t)a.d, c = col - bh * (uint32_t)a.d;
+  const uint32_t b = bh / (uint32_t)a.H, h = bh - b * (uint32_t)a.H;
   l.len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
   l.x = (int64_t)b * a.xs.b + (int64_t)h * a.xs.h + c;
   l.g = (int64_t)b * a.gs.b + (int64_t)h * a.gs.h + c;
@@ -291,50 +260,84 @@ __device__ __forceinline__ Lane lane_of(const ScanArgs& a, uint32_t col) {
   return l;
 }
 
+// L tokens' channels, `stride` elements apart.
+template <typename T, int V, int L>
+__device__ __forceinline__ void fetch(Raw<T, V> (&r)[L], const T* p, int64_t stride) {
+#pragma unroll
+  for (int j = 0; j < L; ++j, p += stride) r[j] = *(const Raw<T, V>*)p;
+}
+
 // The kept state before tile t of column col.
 __device__ __forceinline__ float* state_at(const ScanArgs& a, uint32_t col, int t) {
-  const uint32_t c = col % (uint32_t)a.d, bh = col / (uint32_t)a.d;
+  const uint32_t bh = col / (uint32_t)a.d, c = col - bh * (uint32_t)a.d;
   return a.states + ((int64_t)bh * a.ntiles + t) * a.d + c;
 }
 
-template <typename T, int V, int NT, int L, bool LOG, bool COUPLED, bool CHAIN>
-__global__ __launch_bounds__(NT) void scan_forward_kernel(ScanArgs a, Chain chain, int groups) {
-  using G = Tile<NT, L, V>;
-  using R = typename Raw<T, V>::type;
-  __shared__ Pair totals[2][G::kWaves][G::kWidth];
-  __shared__ float start[G::kWidth];
-  __shared__ int place;
-  const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::kCols, row = tid / G::kCols;
-  int group = blockIdx.x, tile = 0;
-  if constexpr (CHAIN) {
-    if (tid == 0) place = (int)atomicAdd((unsigned*)chain.words, 1u);
-    __syncthreads();
-    tile = place / groups;
-    group = place % groups;
-  }
-  const uint32_t base = (uint32_t)group * G::kWidth;
-  const Lane me = lane_of(a, base + cv * V);
-  const T* x = (const T*)a.x + me.x;
-  const T* g = (const T*)a.g + me.g;
-  T* y = (T*)a.y + me.y;
-  const int stored = me.on ? a.N : 0;
-  // Lanes of the first wave also look after one column each: its carried state.
-  const uint32_t mine = base + tid;
-  const bool keeper = tid < G::kWidth && mine < (uint32_t)a.columns;
-  float h_keep = keeper && a.h0 ? a.h0[mine] : 0.f;
-
-  for (;; ++tile) {
-    const int n0 = tile * kTile + row * L;
-    R xr[L], gr[L];
-    // Tokens behind the sequence's end read its last one and are masked below.
+// The state before the lane's first token, from the one before the tile's.
+template <int V, int WIDTH, bool REVERSE>
+__device__ __forceinline__ void enter(float (&h)[V], const float* start, const Pair (*totals)[WIDTH], int at,
+                                      const Pair (&before)[V]) {
+  const int wave = threadIdx.x / 64;
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const int64_t n = max(min(n0 + j, me.len - 1), 0);
-      gr[j] = *(const R*)(g + n * a.gs.n);
-      xr[j] = *(const R*)(x + n * a.xs.n);
+  for (int v = 0; v < V; ++v) {
+    h[v] = start[at + v];
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) {
+      const int w = REVERSE ? kWaves - 1 - i : i;
+      if (REVERSE ? w > wave : w < wave) h[v] = totals[w][at + v].a * h[v] + totals[w][at + v].s;
     }
+    h[v] = before[v].a * h[v] + before[v].s;
+  }
+}
+
+template <typename T, bool VEC, bool LOG, bool COUPLED, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 3) void scan_forward_kernel(ScanArgs a, Chain chain, int groups) {
+  using G = Geometry<T, VEC>;
+  constexpr int V = G::V, L = G::L, WIDTH = G::WIDTH;
+  __shared__ Pair totals[2][kWaves][WIDTH];
+  __shared__ float start[WIDTH];
+  __shared__ int places[2];
+  const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::COLS * V, row = tid / G::COLS;
+  const int last = a.ntiles - 1;
+  Raw<T, V> xr[L], gr[L];
+  const uint32_t group = blockIdx.x % groups, mine = group * WIDTH + tid;
+  auto draw = [&] { return (int)atomicAdd((unsigned*)(chain.words + group * kCounter), 1u); };
+  int step = 0;
+  if constexpr (CHAIN) {
+    if (tid == 0) places[1] = draw();
+    __syncthreads();
+    step = __builtin_amdgcn_readfirstlane(places[1]);
+    if (step > last) return;
+  }
+  const Lane me = lane_of(a, group * WIDTH + cv);
+  const T* const x = (const T*)a.x + me.x + (int64_t)(row * L) * a.xs.n;
+  const T* const g = (const T*)a.g + me.g + (int64_t)(row * L) * a.gs.n;
+  T* const y = (T*)a.y + me.y + (int64_t)(row * L) * a.ys.n;
+  // Tokens behind the sequence's end read its last one and are masked below.
+  auto load = [&](int tile) {
+    const int first = tile * kTile;
+    if (__all(first + kTile <= me.len)) {
+      fetch(gr, g + first * a.gs.n, a.gs.n);
+      fetch(xr, x + first * a.xs.n, a.xs.n);
+    } else {
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const int64_t n = max(min(first + row * L + j, me.len - 1), 0) - row * L;
+        gr[j] = *(const Raw<T, V>*)(g + n * a.gs.n);
+        xr[j] = *(const Raw<T, V>*)(x + n * a.xs.n);
+      }
+    }
+  };
+  load(step);
+  // Lanes of the first wave also look after one column each: its carried state.
+  const bool keeper = tid < WIDTH && mine < (uint32_t)a.columns;
+  float h_keep = step == 0 && keeper && a.h0 ? a.h0[mine] : 0.f;
+
+  for (int turn = 0;; turn ^= 1) {
+    const int tile = step, n0 = tile * kTile + row * L;
     float f[L][V], u[L][V];
     Pair p[V], before[V];
+#pragma unroll
     for (int v = 0; v < V; ++v) p[v] = {1.f, 0.f};
     const bool full = __all(tile * kTile + kTile <= me.len);
 #pragma unroll
@@ -342,216 +345,224 @@ __global__ __launch_bounds__(NT) void scan_forward_kernel(ScanArgs a, Chain chai
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float rest;
-        gate<LOG>(element<T, V>(gr[j], v), f[j][v], rest);
-        u[j][v] = element<T, V>(xr[j], v);
+        gate<LOG>(gr[j][v], f[j][v], rest);
+        u[j][v] = xr[j][v];
         if (COUPLED) u[j][v] *= rest;
         if (!full && n0 + j >= me.len) f[j][v] = 1.f, u[j][v] = 0.f;
         p[v] = compose(p[v], {f[j][v], u[j][v]});
       }
-    wave_scan<G::kCols, V, false>(p, before);
-    auto& tot = totals[tile & 1];
-    if ((tid & 63) >= 64 - G::kCols)
+    wave_scan<G::COLS, V, false>(p, before);
+    auto& tot = totals[turn];
+    if ((tid & 63) >= 64 - G::COLS)
 #pragma unroll
-      for (int v = 0; v < V; ++v) tot[wave][cv * V + v] = p[v];
+      for (int v = 0; v < V; ++v) tot[wave][cv + v] = p[v];
     __syncthreads();
-    Pair own = {1.f, 0.f};
-    if (tid < G::kWidth) {
-      own = tot[0][tid];
-#pragma unroll
-      for (int i = 1; i < G::kWaves; ++i) own = compose(own, tot[i][tid]);
-    }
-    float h = h_keep;
-    if constexpr (CHAIN) {
-      // The first tile's pair holds the initial state, which no other tile reads.
-      if (tile == 0) own = {0.f, own.a * h + own.s};
-      const Pair b = chain_before<NT, G::kWidth>(chain, tile, a.ntiles - 1, base, own);
-      if (tile > 0) h = b.s;
-      h_keep = tile == 0 ? own.s : own.a * h + own.s;
-    } else {
-      h_keep = own.a * h + own.s;
-    }
+    if (!CHAIN && tile < last) load(tile + 1);
     if (keeper) {
+      Pair own = tot[0][tid];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) own = compose(own, tot[i][tid]);
+      float h = h_keep;
+      if constexpr (CHAIN) {
+        // The first tile's pair holds the initial state, which no other tile reads.
+        if (tile == 0) own = {0.f, own.a * h + own.s};
+        const Pair b = chain_before(chain, tile, last, mine, own);
+        if (tile > 0) h = b.s;
+        h_keep = tile == 0 ? own.s : own.a * h + own.s;
+      } else {
+        h_keep = own.a * h + own.s;
+      }
       start[tid] = h;
       if (a.states) *state_at(a, mine, tile) = h;
-      if (a.hN && tile == a.ntiles - 1) a.hN[mine] = h_keep;
+      if (a.hN && tile == last) a.hN[mine] = h_keep;
     }
     __syncthreads();
-    float at[V];
+    // Drawn only now that this tile waits for nothing any more.
+    int drawn = 0;
+    if (CHAIN && tid == 0) drawn = draw();
+    float h[V];
+    enter<V, WIDTH, false>(h, start, tot, cv, before);
+    T* at = y + (int64_t)(tile * kTile) * a.ys.n;
+    const int stored = me.on ? a.N : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      at[v] = start[cv * V + v];
-      for (int i = 0; i < wave; ++i) at[v] = tot[i][cv * V + v].a * at[v] + tot[i][cv * V + v].s;
-      at[v] = before[v].a * at[v] + before[v].s;
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
+    for (int j = 0; j < L; ++j, at += a.ys.n) {
       float out[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        at[v] = f[j][v] * at[v] + u[j][v];
-        out[v] = !full && n0 + j >= me.len ? 0.f : at[v];
+        h[v] = f[j][v] * h[v] + u[j][v];
+        out[v] = !full && n0 + j >= me.len ? 0.f : h[v];
       }
-      if (n0 + j < stored) put<T, V>(y + (int64_t)(n0 + j) * a.ys.n, out);
+      if (n0 + j < stored) put<V>(at, out);
     }
-    if (CHAIN || tile == a.ntiles - 1) break;
+    ++step;
+    if constexpr (CHAIN) {
+      if (tid == 0) places[turn] = drawn;
+      __syncthreads();
+      step = __builtin_amdgcn_readfirstlane(places[turn]);
+    }
+    if (step > last) break;
+    if (CHAIN) load(step);
   }
 }
 
-template <typename T, int V, int NT, int L, bool LOG, bool COUPLED, bool CHAIN>
-__global__ __launch_bounds__(NT) void scan_backward_kernel(ScanArgs a, Chain chain, int groups) {
-  using G = Tile<NT, L, V>;
-  using R = typename Raw<T, V>::type;
-  __shared__ Pair totals[2][2][G::kWaves][G::kWidth];  // forward and backward pairs
-  __shared__ float start[2][G::kWidth];
-  __shared__ int place;
-  const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::kCols, row = tid / G::kCols;
-  int group = blockIdx.x, step = 0;
+template <typename T, bool VEC, bool LOG, bool COUPLED, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, Chain chain, int groups) {
+  using G = Geometry<T, VEC>;
+  constexpr int V = G::V, L = G::L, WIDTH = G::WIDTH;
+  __shared__ Pair totals[2][2][kWaves][WIDTH];  // of h and of r
+  __shared__ float start[2][2][WIDTH];
+  __shared__ int places[2];
+  const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::COLS * V, row = tid / G::COLS;
+  const int last = a.ntiles - 1;
+  Raw<T, V> xn[L], gr[L], yn[L];
+  const uint32_t group = blockIdx.x % groups, mine = group * WIDTH + tid;
+  auto draw = [&] { return (int)atomicAdd((unsigned*)(chain.words + group * kCounter), 1u); };
+  int step = 0;
   if constexpr (CHAIN) {
-    if (tid == 0) place = (int)atomicAdd((unsigned*)chain.words, 1u);
+    if (tid == 0) places[1] = draw();
     __syncthreads();
-    step = place / groups;
-    group = place % groups;
+    step = __builtin_amdgcn_readfirstlane(places[1]);
+    if (step > last) return;
   }
-  const uint32_t base = (uint32_t)group * G::kWidth;
-  const Lane me = lane_of(a, base + cv * V);
-  const T* x = (const T*)a.x + me.x;
-  const T* g = (const T*)a.g + me.g;
-  const T* dy = (const T*)a.dy + me.y;
-  T* dx = (T*)a.dx + me.x;
-  T* dg = (T*)a.dg + me.g;
-  const int stored = me.on ? a.N : 0;
-  const uint32_t mine = base + tid;
-  const bool keeper = tid < G::kWidth && mine < (uint32_t)a.columns;
-  float r_keep = keeper && a.dhN ? a.dhN[mine] : 0.f;
-
-  for (;; ++step) {
-    const int tile = a.ntiles - 1 - step;
-    const int n0 = tile * kTile + row * L;
-    R xr[L], gr[L], yr[L];
+  const Lane me = lane_of(a, group * WIDTH + cv);
+  const int64_t rx = (int64_t)(row * L) * a.xs.n, rg = (int64_t)(row * L) * a.gs.n, ry = (int64_t)(row * L) * a.ys.n;
+  const T* const x = (const T*)a.x + me.x + rx;
+  const T* const g = (const T*)a.g + me.g + rg;
+  const T* const dy = (const T*)a.dy + me.y + ry;
+  T* const dx = (T*)a.dx + me.x + rx;
+  T* const dg = (T*)a.dg + me.g + rg;
+  auto load = [&](int tile) {
+    const int first = tile * kTile;
+    if (__all(first + kTile <= me.len)) {
+      fetch(gr, g + first * a.gs.n, a.gs.n);
+      fetch(xn, x + first * a.xs.n, a.xs.n);
+      fetch(yn, dy + first * a.ys.n, a.ys.n);
+    } else {
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const int64_t n = max(min(n0 + j, me.len - 1), 0);
-      gr[j] = *(const R*)(g + n * a.gs.n);
-      yr[j] = *(const R*)(dy + n * a.ys.n);
-      xr[j] = *(const R*)(x + n * a.xs.n);
+      for (int j = 0; j < L; ++j) {
+        const int64_t n = max(min(first + row * L + j, me.len - 1), 0) - row * L;
+        gr[j] = *(const Raw<T, V>*)(g + n * a.gs.n);
+        xn[j] = *(const Raw<T, V>*)(x + n * a.xs.n);
+        yn[j] = *(const Raw<T, V>*)(dy + n * a.ys.n);
+      }
     }
-    const float h_keep = keeper ? *state_at(a, mine, tile) : 0.f;
+  };
+  load(last - step);
+  const bool keeper = tid < WIDTH && mine < (uint32_t)a.columns;
+  float r_keep = step == 0 && keeper && a.dhN ? a.dhN[mine] : 0.f;
+
+  for (int turn = 0;; turn ^= 1) {
+    const int tile = last - step, n0 = tile * kTile + row * L;
+    if (keeper) start[turn][0][tid] = *state_at(a, mine, tile);
     const bool full = __all(tile * kTile + kTile <= me.len);
     // Behind the sequence's end gates are 1 and x and dy are 0.
-    constexpr bool BOTH = COUPLED || !LOG;  // 1 - f is needed too
-    float c[L][V];
-    auto decode = [&](int j, int v, float& f, float& rest) {
-      if constexpr (BOTH)
-        unpack_gate(c[j][v], f, rest);
-      else
-        f = c[j][v];
-    };
+    Raw<T, V> xr[L], yr[L];
+    // A logarithmic gate that was cut off at 0, whose slope is 0, has its sign bit set.
+    float f[L][V], rest[L][V];
+    auto gate_at = [&](int j, int v) { return LOG ? fabsf(f[j][v]) : f[j][v]; };
     Pair p[V], hb[V], rb[V];
+#pragma unroll
     for (int v = 0; v < V; ++v) p[v] = {1.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      xr[j] = xn[j];
+      yr[j] = yn[j];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        gate<LOG>(gr[j][v], f[j][v], rest[j][v]);
+        float u = xr[j][v];
+        if (COUPLED) u *= rest[j][v];
+        if (LOG && gr[j][v] > 0.f) f[j][v] = -f[j][v];
+        if (!full && n0 + j >= me.len) f[j][v] = 1.f, u = 0.f;
+        p[v] = compose(p[v], {gate_at(j, v), u});
+      }
+    }
+    auto& tot = totals[turn];
+    Pair q[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) q[v] = {p[v].a, 0.f};
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float e = !full && n0 + j >= me.len ? 0.f : yr[j][v];
+        q[v].s = gate_at(j, v) * (q[v].s + e);
+      }
+    wave_scan<G::COLS, V, false>(p, hb);
+    if ((tid & 63) >= 64 - G::COLS)
+#pragma unroll
+      for (int v = 0; v < V; ++v) tot[0][wave][cv + v] = p[v];
+    wave_scan<G::COLS, V, true>(q, rb);
+    if ((tid & 63) < G::COLS)
+#pragma unroll
+      for (int v = 0; v < V; ++v) tot[1][wave][cv + v] = q[v];
+    __syncthreads();
+    if (!CHAIN && tile > 0) load(tile - 1);
+    if (keeper) {
+      Pair own = tot[1][kWaves - 1][tid];
+#pragma unroll
+      for (int i = kWaves - 2; i >= 0; --i) own = compose(own, tot[1][i][tid]);
+      float r = r_keep;
+      if constexpr (CHAIN) {
+        if (step == 0) own = {0.f, own.a * r + own.s};
+        const Pair b = chain_before(chain, step, last, mine, own);
+        if (step > 0) r = b.s;
+        r_keep = step == 0 ? own.s : own.a * r + own.s;
+      } else {
+        r_keep = own.a * r + own.s;
+      }
+      start[turn][1][tid] = r;
+      if (a.dh0 && tile == 0) a.dh0[mine] = r_keep;
+    }
+    // h before each token needs nothing of the tiles behind.
+    float h[V], hp[L][V];
+    enter<V, WIDTH, false>(h, start[turn][0], tot[0], cv, hb);
 #pragma unroll
     for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float f, rest, u = element<T, V>(xr[j], v);
-        gate<LOG>(element<T, V>(gr[j], v), f, rest);
-        if (COUPLED) u *= rest;
-        c[j][v] = BOTH ? pack_gate(f, rest) : f;
-        if (!full && n0 + j >= me.len) f = 1.f, u = 0.f, c[j][v] = BOTH ? 0.f : 1.f;
-        p[v] = compose(p[v], {f, u});
-        keep(c[j][v]);
+        hp[j][v] = h[v];
+        h[v] = gate_at(j, v) * h[v] + (COUPLED ? rest[j][v] * xr[j][v] : xr[j][v]);
       }
-    auto& tot = totals[step & 1];
-    wave_scan<G::kCols, V, false>(p, hb);
-    if ((tid & 63) >= 64 - G::kCols)
-#pragma unroll
-      for (int v = 0; v < V; ++v) tot[0][wave][cv * V + v] = p[v];
-    for (int v = 0; v < V; ++v) p[v] = {1.f, 0.f};
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float f, rest, e = element<T, V>(yr[j], v);
-        decode(j, v, f, rest);
-        if (!full && n0 + j >= me.len) e = 0.f;
-        p[v] = {p[v].a * f, f * (p[v].s + e)};
-        keep(c[j][v]);
-      }
-    wave_scan<G::kCols, V, true>(p, rb);
-    if ((tid & 63) < G::kCols)
-#pragma unroll
-      for (int v = 0; v < V; ++v) tot[1][wave][cv * V + v] = p[v];
     __syncthreads();
-    Pair own = {1.f, 0.f};
-    if (tid < G::kWidth) {
-      own = tot[1][G::kWaves - 1][tid];
+    int drawn = 0;
+    if (CHAIN && tid == 0) drawn = draw();
+    enter<V, WIDTH, true>(h, start[turn][1], tot[1], cv, rb);
+    T* to_dx = dx + (int64_t)(tile * kTile + L - 1) * a.xs.n;
+    T* to_dg = dg + (int64_t)(tile * kTile + L - 1) * a.gs.n;
+    const int stored = me.on ? a.N : 0;
 #pragma unroll
-      for (int i = G::kWaves - 2; i >= 0; --i) own = compose(own, tot[1][i][tid]);
-    }
-    float r = r_keep;
-    if constexpr (CHAIN) {
-      if (step == 0) own = {0.f, own.a * r + own.s};
-      const Pair b = chain_before<NT, G::kWidth>(chain, step, a.ntiles - 1, base, own);
-      if (step > 0) r = b.s;
-      r_keep = step == 0 ? own.s : own.a * r + own.s;
-    } else {
-      r_keep = own.a * r + own.s;
-    }
-    if (keeper) {
-      start[0][tid] = h_keep;
-      start[1][tid] = r;
-      if (a.dh0 && tile == 0) a.dh0[mine] = r_keep;
-    }
-    __syncthreads();
-    float at[V], dh[L][V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      at[v] = start[1][cv * V + v];
-      for (int i = G::kWaves - 1; i > wave; --i) at[v] = tot[1][i][cv * V + v].a * at[v] + tot[1][i][cv * V + v].s;
-      at[v] = rb[v].a * at[v] + rb[v].s;
-    }
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float f, rest, e = element<T, V>(yr[j], v);
-        decode(j, v, f, rest);
-        if (!full && n0 + j >= me.len) e = 0.f;
-        dh[j][v] = e + at[v];
-        at[v] = f * dh[j][v];
-        keep(c[j][v]);
-      }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      at[v] = start[0][cv * V + v];
-      for (int i = 0; i < wave; ++i) at[v] = tot[0][i][cv * V + v].a * at[v] + tot[0][i][cv * V + v].s;
-      at[v] = hb[v].a * at[v] + hb[v].s;
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
+    for (int j = L - 1; j >= 0; --j, to_dx -= a.xs.n, to_dg -= a.gs.n) {
+      const bool dead = !full && n0 + j >= me.len;
       float gx[V], gg[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float f, rest;
-        decode(j, v, f, rest);
-        const float u = element<T, V>(xr[j], v);
-        gx[v] = COUPLED ? dh[j][v] * rest : dh[j][v];
-        gg[v] = dh[j][v] * (COUPLED ? at[v] - u : at[v]);
-        gg[v] *= LOG ? (element<T, V>(gr[j], v) > 0.f ? 0.f : f) : f * rest;
-        at[v] = f * at[v] + (COUPLED ? rest * u : u);
-        if (!full && n0 + j >= me.len) gx[v] = gg[v] = 0.f;
+        const float dh = (dead ? 0.f : yr[j][v]) + h[v];
+        h[v] = gate_at(j, v) * dh;
+        gx[v] = COUPLED ? dh * rest[j][v] : dh;
+        gg[v] = dh * (COUPLED ? hp[j][v] - xr[j][v] : hp[j][v]);
+        gg[v] *= LOG ? (__float_as_uint(f[j][v]) >> 31 ? 0.f : f[j][v]) : f[j][v] * rest[j][v];
+        if (dead) gx[v] = gg[v] = 0.f;
       }
       if (n0 + j < stored) {
-        put<T, V>(dx + (int64_t)(n0 + j) * a.xs.n, gx);
-        put<T, V>(dg + (int64_t)(n0 + j) * a.gs.n, gg);
+        put<V>(to_dx, gx);
+        put<V>(to_dg, gg);
       }
     }
-    if (CHAIN || tile == 0) break;
+    ++step;
+    if constexpr (CHAIN) {
+      if (tid == 0) places[turn] = drawn;
+      __syncthreads();
+      step = __builtin_amdgcn_readfirstlane(places[turn]);
+    }
+    if (step > last) break;
+    if (CHAIN) load(last - step);
   }
 }
 
 template <typename T, bool LOG, bool COUPLED>
-__global__ __launch_bounds__(256) void scan_step_kernel(StepArgs a) {
-  const long long col = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(StepArgs a) {
+  const long long col = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int hd = a.H * a.d;
   if (col >= (long long)a.B * hd) return;
   const int b = (int)(col / hd), hc = (int)(col % hd);
@@ -577,39 +588,43 @@ hipError_t choose(int dtype, bool log_gate, bool coupled, F f) {
   return dtype == 1 ? flags(uint16_t()) : flags(float());
 }
 
-// Few columns: a tile a workgroup.
+// Few columns: workgroups share the tiles of a column.
 bool chained(const ScanArgs& a) {
-  return a.ntiles > 1 && a.columns < 65536 && a.columns * a.ntiles <= INT32_MAX;
+  return a.ntiles > 1 && a.columns < 32768 && a.columns * a.ntiles <= INT32_MAX / 2;
 }
 
-// Zeroes the counter and unsets the words of a chain in the workspace.
-hipError_t start_chain(const ScanArgs& a, void* ws, Chain* c, hipStream_t s) {
+// Zeroes the counters and unsets the pairs of a chain in the workspace.
+hipError_t start_chain(const ScanArgs& a, int groups, void* ws, Chain* c, hipStream_t s) {
   c->words = (uint64_t*)ws;
   c->columns = a.columns;
-  const long long n = chain_layout(a.ntiles, a.columns, c->level);
-  scan_fill_kernel<<<dim3((unsigned)((n + kFillThreads - 1) / kFillThreads)), dim3(kFillThreads), 0, s>>>(c->words, n);
+  const long long n = chain_layout(a.ntiles, a.columns, groups, c->level);
+  scan_fill_kernel<<<dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(
+      c->words, (long long)groups * kCounter, n);
   return hipGetLastError();
 }
 
-template <bool BACKWARD, typename T, int V, int NT, int L, bool LOG, bool COUPLED>
+// Workgroups of a chain launch: about what the chip's 256 CUs hold at once.
+constexpr int kResident = 256 * 4;
+
+int groups_of(const ScanArgs& a, int width) { return (int)((a.columns + width - 1) / width); }
+
+template <bool BACKWARD, typename T, bool VEC, bool LOG, bool COUPLED>
 hipError_t launch(const ScanArgs& a, void* ws, hipStream_t s) {
-  const int groups = (int)((a.columns + Tile<NT, L, V>::kWidth - 1) / Tile<NT, L, V>::kWidth);
+  constexpr int WIDTH = Geometry<T, VEC>::WIDTH;
+  const int groups = groups_of(a, WIDTH);
+  auto* const chain_form =
+      BACKWARD ? scan_backward_kernel<T, VEC, LOG, COUPLED, true> : scan_forward_kernel<T, VEC, LOG, COUPLED, true>;
+  auto* const loop_form =
+      BACKWARD ? scan_backward_kernel<T, VEC, LOG, COUPLED, false> : scan_forward_kernel<T, VEC, LOG, COUPLED, false>;
   Chain c = {};
-  if (chained(a)) {
-    const hipError_t e = start_chain(a, ws, &c, s);
-    if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((long long)groups * a.ntiles));
-    if constexpr (BACKWARD)
-      scan_backward_kernel<T, V, NT, L, LOG, COUPLED, true><<<grid, dim3(NT), 0, s>>>(a, c, groups);
-    else
-      scan_forward_kernel<T, V, NT, L, LOG, COUPLED, true><<<grid, dim3(NT), 0, s>>>(a, c, groups);
-  } else {
-    const dim3 grid((unsigned)groups);
-    if constexpr (BACKWARD)
-      scan_backward_kernel<T, V, NT, L, LOG, COUPLED, false><<<grid, dim3(NT), 0, s>>>(a, c, groups);
-    else
-      scan_forward_kernel<T, V, NT, L, LOG, COUPLED, false><<<grid, dim3(NT), 0, s>>>(a, c, groups);
+  if (!chained(a)) {
+    loop_form<<<dim3(groups), dim3(kThreads), 0, s>>>(a, c, groups);
+    return hipGetLastError();
   }
+  const hipError_t e = start_chain(a, groups, ws, &c, s);
+  if (e != hipSuccess) return e;
+  const int share = (kResident + groups - 1) / groups;  // workgroups to a group
+  chain_form<<<dim3((unsigned)(groups * (share < a.ntiles ? share : a.ntiles))), dim3(kThreads), 0, s>>>(a, c, groups);
   return hipGetLastError();
 }
 
@@ -618,8 +633,7 @@ hipError_t launch_scan(const ScanArgs& a, void* ws, hipStream_t s) {
   return choose(a.dtype, a.log_gate, a.coupled, [&](auto t, auto lg, auto cp) {
     using T = decltype(t);
     constexpr bool LOG = decltype(lg)::value, COUPLED = decltype(cp)::value;
-    if (a.vec) return launch<BACKWARD, T, 16 / sizeof(T), 512, 4, LOG, COUPLED>(a, ws, s);
-    return launch<BACKWARD, T, 1, 512, 16, LOG, COUPLED>(a, ws, s);
+    return a.vec ? launch<BACKWARD, T, true, LOG, COUPLED>(a, ws, s) : launch<BACKWARD, T, false, LOG, COUPLED>(a, ws, s);
   });
 }
 
@@ -627,8 +641,9 @@ hipError_t launch_scan(const ScanArgs& a, void* ws, hipStream_t s) {
 
 size_t scan_workspace(const ScanArgs& a) {
   if (!chained(a)) return 0;
-  long long level[3];
-  return (size_t)chain_layout(a.ntiles, a.columns, level) * sizeof(uint64_t);
+  long long level[kLevels];
+  // Groups are narrowest, and so most, at 32 columns.
+  return (size_t)chain_layout(a.ntiles, a.columns, groups_of(a, 32), level) * sizeof(uint64_t);
 }
 
 hipError_t launch_scan_forward(const ScanArgs& a, void* ws, hipStream_t s) { return launch_scan<false>(a, ws, s); }
@@ -639,7 +654,7 @@ hipError_t launch_scan_step(const StepArgs& a, hipStream_t s) {
   const long long n = (long long)a.B * a.H * a.d;
   return choose(a.dtype, a.log_gate, a.coupled, [&](auto t, auto lg, auto cp) {
     scan_step_kernel<decltype(t), decltype(lg)::value, decltype(cp)::value>
-        <<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s>>>(a);
+        <<<dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   });
 }

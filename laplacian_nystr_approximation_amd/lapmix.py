@@ -21,7 +21,7 @@ from .lapnys import LAPNYS_BF16, LAPNYS_F32, _check, _lib, _stream as _given_str
 LAPMIX_E4M3 = 2
 LAPMIX_GATE_LOG = 1
 LAPMIX_COUPLED = 2
-LAPMIX_SCAN_TILE = 256
+LAPMIX_SCAN_TILE = 128
 
 _SIZES = {LAPNYS_F32: 4, LAPNYS_BF16: 2, LAPMIX_E4M3: 1}
 _NAMES = {"f32": LAPNYS_F32, "bf16": LAPNYS_BF16, "e4m3": LAPMIX_E4M3}

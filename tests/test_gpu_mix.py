@@ -127,10 +127,11 @@ class Scan:
             worst[name] = round(_check(name, _np(t), w[name], w["e_" + name], h), 3)
         # The kept states are the tiles' first h_{t-1}.
         B, H, N, d = self.shape
+        T = self.L.LAPMIX_SCAN_TILE
         st = _np(self.states).reshape(B, H, -1, d)
         first = np.zeros((B, H, 1, d)) if self.h0 is None else _np(self.h0)[:, :, None]
-        before = np.concatenate([first, w["h"][:, :, 255:N - 1:256]], axis=2)
-        e = np.concatenate([np.zeros((B, H, 1, d)), w["e_h"][:, :, 255:N - 1:256]], axis=2)
+        before = np.concatenate([first, w["h"][:, :, T - 1:N - 1:T]], axis=2)
+        e = np.concatenate([np.zeros((B, H, 1, d)), w["e_h"][:, :, T - 1:N - 1:T]], axis=2)
         _check("states", st, before, e, HALF["f32"])
         _say(f"[scan] {self.shape} {self.dtype} {self.layout} worst/tolerance {worst}")
 

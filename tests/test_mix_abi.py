@@ -199,8 +199,8 @@ def test_norm_buffers_refused():
 
 def test_sizes():
     p = _scan()
-    assert L.lapmix_scan_states_size(p) == 2 * 3 * 3 * 64 * 4  # three tiles of 256 tokens
-    assert L.lapmix_scan_states_size(_scan(N=256)) == 2 * 3 * 64 * 4
+    assert L.lapmix_scan_states_size(p) == 2 * 3 * -(-600 // L.LAPMIX_SCAN_TILE) * 64 * 4
+    assert L.lapmix_scan_states_size(_scan(N=L.LAPMIX_SCAN_TILE)) == 2 * 3 * 64 * 4
     assert L.lapmix_scan_workspace_size(p) % 256 == 0
     assert L.lapmix_norm_workspace_size(_norm()) >= 192 * 4
 
