@@ -7,6 +7,7 @@
 // way, the next row's already on their way while a row is worked on; each
 // workgroup takes every gridDim-th row and keeps its part of dw in registers, and
 // a second kernel adds the parts in a fixed order.  Both are bound by HBM.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "lapmix_internal.hpp"
@@ -294,20 +295,32 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
   }
 }
 
-// Adds the parts of dw: a workgroup takes 64 columns, its waves every 4th part each.
-__global__ __launch_bounds__(kNarrow) void norm_weight_kernel(NormArgs a) {
-  constexpr int WAVES = kNarrow / 64;
-  __shared__ float sums[WAVES][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int c = blockIdx.x * 64 + lane;
+// Adds the parts of dw: a workgroup takes 32 columns, its rows of 32 lanes every 32nd
+// part each, kAtOnce of them under way at a time.
+constexpr int kAtOnce = 8;
+
+__global__ __launch_bounds__(kWide) void norm_weight_kernel(NormArgs a) {
+  constexpr int ROWS = kWide / 32;
+  __shared__ float sums[ROWS][33];
+  const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
+  const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
   if (c < a.C)
-    for (int i = wave; i < a.parts; i += WAVES) sum += a.part[(long long)i * a.C + c];
-  sums[wave][lane] = sum;
+    for (int i = row; i < a.parts; i += ROWS * kAtOnce) {
+      float v[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) v[k] = i + k * ROWS < a.parts ? a.part[(long long)(i + k * ROWS) * a.C + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) sum += v[k];
+    }
+  sums[row][lane] = sum;
   __syncthreads();
-  if (wave || c >= a.C) return;
-  for (int i = 1; i < WAVES; ++i) sum += sums[i][lane];
-  a.dw[c] = sum;
+  // Rows of lanes now take a column each.
+  float v[1] = {sums[lane][row]};
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) v[0] += __shfl_xor(v[0], m);
+  const int out = blockIdx.x * 32 + row;
+  if (lane == 0 && out < a.C) a.dw[out] = v[0];
 }
 
 // How rows of C columns are laid on lanes: TPR lanes of a workgroup of kNarrow, or
@@ -356,8 +369,9 @@ void with_types(const NormArgs& a, F f) {
 // Enough workgroups to fill the chip, and rows enough for each that the parts of
 // dw are small beside the rows.
 static int norm_groups(long long rows, const Shape& shape) {
-  const long long n = (rows + shape.rows() - 1) / shape.rows();
-  return (int)(n < 1024 ? n : 1024);
+  static const int G = getenv("LM_G") ? atoi(getenv("LM_G")) : 1024, D = getenv("LM_D") ? atoi(getenv("LM_D")) : 1;
+  const long long n = (rows + shape.rows() * D - 1) / (shape.rows() * D);
+  return (int)(n < G ? n : G);
 }
 
 size_t norm_part_count(const NormArgs& a) {
@@ -396,7 +410,7 @@ hipError_t launch_norm_backward(const NormArgs& args, hipStream_t s) {
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
-  norm_weight_kernel<<<dim3((unsigned)((a.C + 63) / 64)), dim3(kNarrow), 0, s>>>(a);
+  norm_weight_kernel<<<dim3((unsigned)((a.C + 31) / 32)), dim3(kWide), 0, s>>>(a);
   return hipGetLastError();
 }
 

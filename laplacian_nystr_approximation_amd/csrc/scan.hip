@@ -54,9 +54,17 @@ constexpr uint64_t kUnset = ~(uint64_t)0;
 // Words of a counter: each has 256 bytes of its own.
 constexpr int kCounter = 32;
 
+// A lane writes kFillEach pairs of words.
+constexpr int kFillEach = 4;
+
 __global__ __launch_bounds__(kThreads) void scan_fill_kernel(uint64_t* words, long long counters, long long n) {
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i < n) words[i] = i < counters ? 0 : kUnset;
+  const long long first = (long long)blockIdx.x * (kThreads * kFillEach) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kFillEach; ++k) {
+    const long long i = 2 * (first + k * kThreads);
+    const uint32_t v = i < counters ? 0 : (uint32_t)kUnset;
+    if (i < n) *(u32x4*)(words + i) = (u32x4){v, v, v, v};
+  }
 }
 
 __device__ __forceinline__ void publish(uint64_t* at, Pair p) {
@@ -69,21 +77,15 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* at) {
   return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ bool unset(uint64_t w) { return (uint32_t)w == (uint32_t)kUnset; }
-
-__device__ __forceinline__ Pair pair_of(uint64_t w) {
-  return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
-}
-
 // Waits until a pair that was seen as `w` is there.  The bound on the polls only
 // matters if a workspace is written from outside while the kernel runs: the
 // results are then NaN.
 __device__ __forceinline__ Pair wait_for(const uint64_t* at, uint64_t w) {
-  for (int tries = 0; unset(w) && tries < (1 << 20); ++tries) {
+  for (int tries = 0; (uint32_t)w == (uint32_t)kUnset && tries < (1 << 20); ++tries) {
     __builtin_amdgcn_s_sleep(1);
     w = peek(at);
   }
-  return pair_of(w);
+  return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
 }
 
 // The words of a launch's chain: the groups' counters, then for each level [places][columns].
@@ -100,55 +102,71 @@ long long chain_layout(int ntiles, long long columns, long long groups, long lon
     at += n * columns;
     n /= kFan;
   }
-  return at;
+  return (at + 1) & ~1ll;  // filled two at a time
 }
 
-// Publishes the pair `own` of place p in one column and returns the pair of
-// everything before it.  The first levels' pairs are asked for together.
-__device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, uint32_t col, Pair own) {
-  constexpr int FIRST = 2;
-  uint64_t* const w = c.words + col;
-  if (p < last) publish(w + c.level[0] + (long long)p * c.columns, own);
-  uint64_t seen[FIRST][kFan - 1];
+// The pair of everything before place p in the WIDTH columns from `base` on, for the
+// lanes tid < WIDTH, which hand in their columns' own pairs.  All of a workgroup's
+// lanes take part: each waits for a few of a column's pairs (SLOTS lanes a column).
+template <int WIDTH>
+__device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, uint32_t base, Pair own) {
+  constexpr int SLOTS = kThreads / WIDTH, EACH = kFan / SLOTS, FIRST = 3;
+  __shared__ Pair parts[kLevels][SLOTS][WIDTH];
+  const int slot = threadIdx.x / WIDTH, lane = threadIdx.x % WIDTH;
+  const bool on = base + lane < (uint64_t)c.columns;
+  uint64_t* const words = c.words + (on ? base + lane : 0);
+  auto at = [&](int level, int place) { return words + c.level[level] + place * c.columns; };
+  const bool publishes = slot == 0 && on && p < last;
+  if (publishes) publish(at(0, p), own);
+  // The first levels' pairs are asked for together.
+  uint64_t seen[FIRST][EACH];
   int q = p;
 #pragma unroll
-  for (int l = 0; l < FIRST; ++l, q /= kFan) {
-    const uint64_t* at = w + c.level[l] + (long long)(q - q % kFan) * c.columns;
+  for (int l = 0; l < FIRST; ++l, q /= kFan)
 #pragma unroll
-    for (int i = 0; i < kFan - 1; ++i) seen[l][i] = i < q % kFan ? peek(at + i * c.columns) : 0;
-  }
-  Pair before = {1.f, 0.f};
+    for (int i = 0; i < EACH; ++i) {
+      const int k = slot * EACH + i;
+      seen[l][i] = on && k < q % kFan ? peek(at(l, q - q % kFan + k)) : 0;
+    }
   bool full = true;  // the levels so far end with this place
+  int levels = 0;
   q = p;
 #pragma unroll
   for (int l = 0; l < kLevels; ++l, q /= kFan) {
+    if (q == 0) break;
     const bool top = l == kLevels - 1;
-    const int n = top ? q : q % kFan;
-    const uint64_t* at = w + c.level[l] + (long long)(q - n) * c.columns;
+    const int n = top ? q : q % kFan, first = q - n;
     Pair sum = {1.f, 0.f};
     if (l < FIRST) {
 #pragma unroll
-      for (int i = 0; i < kFan - 1; ++i)
-        if (i < n) sum = compose(sum, wait_for(at + i * c.columns, seen[l][i]));
-    } else {
-      for (int i0 = 0; i0 < n; i0 += kFan) {
-        uint64_t v[kFan];
-#pragma unroll
-        for (int i = 0; i < kFan; ++i) v[i] = i0 + i < n ? peek(at + (i0 + i) * c.columns) : 0;
-#pragma unroll
-        for (int i = 0; i < kFan; ++i)
-          if (i0 + i < n) sum = compose(sum, wait_for(at + (i0 + i) * c.columns, v[i]));
+      for (int i = 0; i < EACH; ++i) {
+        const int k = slot * EACH + i;
+        if (on && k < n) sum = compose(sum, wait_for(at(l, first + k), seen[l][i]));
       }
+    } else {
+      const int each = (n + SLOTS - 1) / SLOTS;
+      for (int k = slot * each; on && k < min(n, slot * each + each); ++k)
+        sum = compose(sum, wait_for(at(l, first + k), peek(at(l, first + k))));
     }
+    parts[l][slot][lane] = sum;
+    levels = l + 1;
     // The next level's pair goes out before that level is waited for.
     full = full && !top && n == kFan - 1;
     if (full) {
-      own = compose(sum, own);
-      if (p < last) publish(w + c.level[l + 1] + (long long)(q / kFan) * c.columns, own);
+      __syncthreads();
+      if (slot == 0) {
+        Pair all = {1.f, 0.f};
+        for (int i = 0; i < SLOTS; ++i) all = compose(all, parts[l][i][lane]);
+        own = compose(all, own);
+        if (publishes) publish(at(l + 1, q / kFan), own);
+      }
     }
-    before = compose(sum, before);
-    if (q < kFan) break;
   }
+  __syncthreads();
+  Pair before = {1.f, 0.f};
+  if (slot == 0)
+    for (int l = levels - 1; l >= 0; --l)
+      for (int i = 0; i < SLOTS; ++i) before = compose(before, parts[l][i][lane]);
   return before;
 }
 
@@ -189,6 +207,14 @@ struct Raw<uint16_t, 4> {
     return __uint_as_float(v % 2 ? e[v / 2] & 0xffff0000u : e[v / 2] << 16);
   }
 };
+
+// Keeps raw values in their registers: what is derived from them before is derived
+// again behind, and takes no registers in between.
+template <typename T, int V, int L>
+__device__ __forceinline__ void keep(Raw<T, V> (&r)[L]) {
+#pragma unroll
+  for (int j = 0; j < L; ++j) asm volatile("" : "+v"(r[j].e));
+}
 
 template <int V, typename T>
 __device__ __forceinline__ void put(T* at, const float* v) {
@@ -242,9 +268,10 @@ __device__ __forceinline__ void wave_scan(Pair (&p)[V], Pair (&before)[V]) {
 
 // What a lane is in charge of.
 struct Lane {
-  bool on;       // its columns exist
-  int len;       // tokens of the sequence
+  bool on;          // its columns exist
+  int len;          // tokens of the sequence
   int64_t x, g, y;  // offsets of token 0
+  int64_t state;    // offset of the first kept state
 };
 
 __device__ __forceinline__ Lane lane_of(const ScanArgs& a, uint32_t col) {
@@ -257,6 +284,7 @@ __device__ __forceinline__ Lane lane_of(const ScanArgs& a, uint32_t col) {
   l.x = (int64_t)b * a.xs.b + (int64_t)h * a.xs.h + c;
   l.g = (int64_t)b * a.gs.b + (int64_t)h * a.gs.h + c;
   l.y = (int64_t)b * a.ys.b + (int64_t)h * a.ys.h + c;
+  l.state = (int64_t)bh * a.ntiles * a.d + c;
   return l;
 }
 
@@ -267,90 +295,97 @@ __device__ __forceinline__ void fetch(Raw<T, V> (&r)[L], const T* p, int64_t str
   for (int j = 0; j < L; ++j, p += stride) r[j] = *(const Raw<T, V>*)p;
 }
 
-// The kept state before tile t of column col.
-__device__ __forceinline__ float* state_at(const ScanArgs& a, uint32_t col, int t) {
-  const uint32_t bh = col / (uint32_t)a.d, c = col - bh * (uint32_t)a.d;
-  return a.states + ((int64_t)bh * a.ntiles + t) * a.d + c;
+// The same from the tokens n0 .. n0 + L - 1 of a sequence that may end before: tokens
+// behind its end read its last one (an empty one's first) and are masked by the caller.
+template <typename T, int V, int L>
+__device__ __forceinline__ void fetch_to(Raw<T, V> (&r)[L], const T* p, int64_t stride, int n0, int len) {
+#pragma unroll
+  for (int j = 0; j < L; ++j) r[j] = *(const Raw<T, V>*)(p + (int64_t)(max(min(n0 + j, len - 1), 0) - n0) * stride);
 }
 
-// The state before the lane's first token, from the one before the tile's.
-template <int V, int WIDTH, bool REVERSE>
-__device__ __forceinline__ void enter(float (&h)[V], const float* start, const Pair (*totals)[WIDTH], int at,
-                                      const Pair (&before)[V]) {
-  const int wave = threadIdx.x / 64;
+// Calls f with whether every token of a wave's lanes exists, as a compile-time value.
+template <typename F>
+__device__ __forceinline__ void when(bool full, F f) {
+  if (full)
+    f(std::true_type());
+  else
+    f(std::false_type());
+}
+
+// Where the waves enter a tile: the state before the first (or REVERSE: behind the
+// last) wave's tokens and the waves' pairs give those of the others.  Returns the
+// state that the tile passes on.
+template <int WIDTH, bool REVERSE>
+__device__ __forceinline__ float enter_waves(float (*start)[WIDTH], const Pair (*totals)[WIDTH], float h) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = start[at + v];
-#pragma unroll
-    for (int i = 0; i < kWaves - 1; ++i) {
-      const int w = REVERSE ? kWaves - 1 - i : i;
-      if (REVERSE ? w > wave : w < wave) h[v] = totals[w][at + v].a * h[v] + totals[w][at + v].s;
-    }
-    h[v] = before[v].a * h[v] + before[v].s;
+  for (int i = 0; i < kWaves; ++i) {
+    const int w = REVERSE ? kWaves - 1 - i : i;
+    start[w][threadIdx.x] = h;
+    h = totals[w][threadIdx.x].a * h + totals[w][threadIdx.x].s;
   }
+  return h;
 }
 
 template <typename T, bool VEC, bool LOG, bool COUPLED, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 3) void scan_forward_kernel(ScanArgs a, Chain chain, int groups) {
+__global__ __launch_bounds__(kThreads, CHAIN ? 3 : 2) void scan_forward_kernel(ScanArgs a, Chain chain, int groups) {
   using G = Geometry<T, VEC>;
   constexpr int V = G::V, L = G::L, WIDTH = G::WIDTH;
   __shared__ Pair totals[2][kWaves][WIDTH];
-  __shared__ float start[WIDTH];
+  __shared__ float start[kWaves][WIDTH];
   __shared__ int places[2];
   const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::COLS * V, row = tid / G::COLS;
   const int last = a.ntiles - 1;
-  Raw<T, V> xr[L], gr[L];
   const uint32_t group = blockIdx.x % groups, mine = group * WIDTH + tid;
   auto draw = [&] { return (int)atomicAdd((unsigned*)(chain.words + group * kCounter), 1u); };
-  int step = 0;
+  int tile = 0;
   if constexpr (CHAIN) {
     if (tid == 0) places[1] = draw();
     __syncthreads();
-    step = __builtin_amdgcn_readfirstlane(places[1]);
-    if (step > last) return;
+    tile = __builtin_amdgcn_readfirstlane(places[1]);
+    if (tile > last) return;
   }
   const Lane me = lane_of(a, group * WIDTH + cv);
   const T* const x = (const T*)a.x + me.x + (int64_t)(row * L) * a.xs.n;
   const T* const g = (const T*)a.g + me.g + (int64_t)(row * L) * a.gs.n;
   T* const y = (T*)a.y + me.y + (int64_t)(row * L) * a.ys.n;
-  // Tokens behind the sequence's end read its last one and are masked below.
-  auto load = [&](int tile) {
-    const int first = tile * kTile;
-    if (__all(first + kTile <= me.len)) {
+  Raw<T, V> xr[L], gr[L];
+  auto is_full = [&](int t) { return __all(me.on && t * kTile + kTile <= me.len); };
+  auto load = [&](int t) {
+    const int64_t first = t * kTile;
+    if (is_full(t)) {
       fetch(gr, g + first * a.gs.n, a.gs.n);
       fetch(xr, x + first * a.xs.n, a.xs.n);
     } else {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int64_t n = max(min(first + row * L + j, me.len - 1), 0) - row * L;
-        gr[j] = *(const Raw<T, V>*)(g + n * a.gs.n);
-        xr[j] = *(const Raw<T, V>*)(x + n * a.xs.n);
-      }
+      fetch_to(gr, g + first * a.gs.n, a.gs.n, t * kTile + row * L, me.len);
+      fetch_to(xr, x + first * a.xs.n, a.xs.n, t * kTile + row * L, me.len);
     }
   };
-  load(step);
+  load(tile);
   // Lanes of the first wave also look after one column each: its carried state.
   const bool keeper = tid < WIDTH && mine < (uint32_t)a.columns;
-  float h_keep = step == 0 && keeper && a.h0 ? a.h0[mine] : 0.f;
+  float carried = tile == 0 && keeper && a.h0 ? a.h0[mine] : 0.f;
 
   for (int turn = 0;; turn ^= 1) {
-    const int tile = step, n0 = tile * kTile + row * L;
+    const int n0 = tile * kTile + row * L;
+    const bool full = is_full(tile);
+    keep(gr);
+    keep(xr);
     float f[L][V], u[L][V];
     Pair p[V], before[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = {1.f, 0.f};
-    const bool full = __all(tile * kTile + kTile <= me.len);
+    when(full, [&](auto all) {
 #pragma unroll
-    for (int j = 0; j < L; ++j)
+      for (int j = 0; j < L; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float rest;
-        gate<LOG>(gr[j][v], f[j][v], rest);
-        u[j][v] = xr[j][v];
-        if (COUPLED) u[j][v] *= rest;
-        if (!full && n0 + j >= me.len) f[j][v] = 1.f, u[j][v] = 0.f;
-        p[v] = compose(p[v], {f[j][v], u[j][v]});
-      }
+        for (int v = 0; v < V; ++v) {
+          float rest;
+          gate<LOG>(gr[j][v], f[j][v], rest);
+          u[j][v] = COUPLED ? rest * xr[j][v] : xr[j][v];
+          if (!all && n0 + j >= me.len) f[j][v] = 1.f, u[j][v] = 0.f;
+          p[v] = compose(p[v], {f[j][v], u[j][v]});
+        }
+    });
     wave_scan<G::COLS, V, false>(p, before);
     auto& tot = totals[turn];
     if ((tid & 63) >= 64 - G::COLS)
@@ -358,50 +393,51 @@ __global__ __launch_bounds__(kThreads, 3) void scan_forward_kernel(ScanArgs a, C
       for (int v = 0; v < V; ++v) tot[wave][cv + v] = p[v];
     __syncthreads();
     if (!CHAIN && tile < last) load(tile + 1);
-    if (keeper) {
-      Pair own = tot[0][tid];
+    if constexpr (CHAIN) {
+      Pair own = {1.f, 0.f};
+      if (keeper)
 #pragma unroll
-      for (int i = 1; i < kWaves; ++i) own = compose(own, tot[i][tid]);
-      float h = h_keep;
-      if constexpr (CHAIN) {
-        // The first tile's pair holds the initial state, which no other tile reads.
-        if (tile == 0) own = {0.f, own.a * h + own.s};
-        const Pair b = chain_before(chain, tile, last, mine, own);
-        if (tile > 0) h = b.s;
-        h_keep = tile == 0 ? own.s : own.a * h + own.s;
-      } else {
-        h_keep = own.a * h + own.s;
-      }
-      start[tid] = h;
-      if (a.states) *state_at(a, mine, tile) = h;
-      if (a.hN && tile == last) a.hN[mine] = h_keep;
+        for (int i = 0; i < kWaves; ++i) own = compose(own, tot[i][tid]);
+      // The first tile's pair holds the initial state, which no other tile reads.
+      if (tile == 0) own = {0.f, own.a * carried + own.s};
+      const Pair b = chain_before<WIDTH>(chain, tile, last, group * WIDTH, own);
+      if (tile > 0) carried = b.s;
+    }
+    if (keeper) {
+      carried = enter_waves<WIDTH, false>(start, tot, carried);
+      if (a.hN && tile == last) a.hN[mine] = carried;
     }
     __syncthreads();
     // Drawn only now that this tile waits for nothing any more.
     int drawn = 0;
     if (CHAIN && tid == 0) drawn = draw();
     float h[V];
-    enter<V, WIDTH, false>(h, start, tot, cv, before);
-    T* at = y + (int64_t)(tile * kTile) * a.ys.n;
-    const int stored = me.on ? a.N : 0;
 #pragma unroll
-    for (int j = 0; j < L; ++j, at += a.ys.n) {
-      float out[V];
+    for (int v = 0; v < V; ++v) h[v] = before[v].a * start[wave][cv + v] + before[v].s;
+    if (a.states && row == 0 && me.on)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = f[j][v] * h[v] + u[j][v];
-        out[v] = !full && n0 + j >= me.len ? 0.f : h[v];
+      for (int v = 0; v < V; ++v) a.states[me.state + (int64_t)tile * a.d + v] = h[v];
+    when(full, [&](auto all) {
+      T* at = y + (int64_t)(tile * kTile) * a.ys.n;
+#pragma unroll
+      for (int j = 0; j < L; ++j, at += a.ys.n) {
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = f[j][v] * h[v] + u[j][v];
+          out[v] = !all && n0 + j >= me.len ? 0.f : h[v];
+        }
+        if (all || (me.on && n0 + j < a.N)) put<V>(at, out);
       }
-      if (n0 + j < stored) put<V>(at, out);
-    }
-    ++step;
+    });
+    ++tile;
     if constexpr (CHAIN) {
       if (tid == 0) places[turn] = drawn;
       __syncthreads();
-      step = __builtin_amdgcn_readfirstlane(places[turn]);
+      tile = __builtin_amdgcn_readfirstlane(places[turn]);
     }
-    if (step > last) break;
-    if (CHAIN) load(step);
+    if (tile > last) break;
+    if (CHAIN) load(tile);
   }
 }
 
@@ -409,15 +445,14 @@ template <typename T, bool VEC, bool LOG, bool COUPLED, bool CHAIN>
 __global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, Chain chain, int groups) {
   using G = Geometry<T, VEC>;
   constexpr int V = G::V, L = G::L, WIDTH = G::WIDTH;
-  __shared__ Pair totals[2][2][kWaves][WIDTH];  // of h and of r
-  __shared__ float start[2][2][WIDTH];
+  __shared__ Pair totals[2][2][kWaves][WIDTH];   // of h and of r
+  __shared__ float start[2][2][kWaves][WIDTH];
   __shared__ int places[2];
   const int tid = threadIdx.x, wave = tid / 64, cv = tid % G::COLS * V, row = tid / G::COLS;
   const int last = a.ntiles - 1;
-  Raw<T, V> xn[L], gr[L], yn[L];
   const uint32_t group = blockIdx.x % groups, mine = group * WIDTH + tid;
   auto draw = [&] { return (int)atomicAdd((unsigned*)(chain.words + group * kCounter), 1u); };
-  int step = 0;
+  int step = 0;  // tiles from the last one
   if constexpr (CHAIN) {
     if (tid == 0) places[1] = draw();
     __syncthreads();
@@ -431,63 +466,65 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, 
   const T* const dy = (const T*)a.dy + me.y + ry;
   T* const dx = (T*)a.dx + me.x + rx;
   T* const dg = (T*)a.dg + me.g + rg;
-  auto load = [&](int tile) {
-    const int first = tile * kTile;
-    if (__all(first + kTile <= me.len)) {
+  Raw<T, V> xn[L], gr[L], yn[L];
+  auto is_full = [&](int t) { return __all(me.on && t * kTile + kTile <= me.len); };
+  auto load = [&](int t) {
+    const int64_t first = t * kTile;
+    if (is_full(t)) {
       fetch(gr, g + first * a.gs.n, a.gs.n);
       fetch(xn, x + first * a.xs.n, a.xs.n);
       fetch(yn, dy + first * a.ys.n, a.ys.n);
     } else {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int64_t n = max(min(first + row * L + j, me.len - 1), 0) - row * L;
-        gr[j] = *(const Raw<T, V>*)(g + n * a.gs.n);
-        xn[j] = *(const Raw<T, V>*)(x + n * a.xs.n);
-        yn[j] = *(const Raw<T, V>*)(dy + n * a.ys.n);
-      }
+      fetch_to(gr, g + first * a.gs.n, a.gs.n, t * kTile + row * L, me.len);
+      fetch_to(xn, x + first * a.xs.n, a.xs.n, t * kTile + row * L, me.len);
+      fetch_to(yn, dy + first * a.ys.n, a.ys.n, t * kTile + row * L, me.len);
     }
   };
   load(last - step);
   const bool keeper = tid < WIDTH && mine < (uint32_t)a.columns;
-  float r_keep = step == 0 && keeper && a.dhN ? a.dhN[mine] : 0.f;
+  const float* const kept = a.states + (keeper ? lane_of(a, mine).state : 0);
+  float carried = step == 0 && keeper && a.dhN ? a.dhN[mine] : 0.f;
 
   for (int turn = 0;; turn ^= 1) {
     const int tile = last - step, n0 = tile * kTile + row * L;
-    if (keeper) start[turn][0][tid] = *state_at(a, mine, tile);
-    const bool full = __all(tile * kTile + kTile <= me.len);
+    const float h_start = keeper ? kept[(int64_t)tile * a.d] : 0.f;
+    const bool full = is_full(tile);
+    keep(gr);
+    keep(xn);
+    keep(yn);
     // Behind the sequence's end gates are 1 and x and dy are 0.
     Raw<T, V> xr[L], yr[L];
     // A logarithmic gate that was cut off at 0, whose slope is 0, has its sign bit set.
     float f[L][V], rest[L][V];
     auto gate_at = [&](int j, int v) { return LOG ? fabsf(f[j][v]) : f[j][v]; };
-    Pair p[V], hb[V], rb[V];
+    Pair p[V], q[V], hb[V], rb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) p[v] = {1.f, 0.f};
+    when(full, [&](auto all) {
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      xr[j] = xn[j];
-      yr[j] = yn[j];
+      for (int j = 0; j < L; ++j) {
+        xr[j] = xn[j];
+        yr[j] = yn[j];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate<LOG>(gr[j][v], f[j][v], rest[j][v]);
-        float u = xr[j][v];
-        if (COUPLED) u *= rest[j][v];
-        if (LOG && gr[j][v] > 0.f) f[j][v] = -f[j][v];
-        if (!full && n0 + j >= me.len) f[j][v] = 1.f, u = 0.f;
-        p[v] = compose(p[v], {gate_at(j, v), u});
+        for (int v = 0; v < V; ++v) {
+          gate<LOG>(gr[j][v], f[j][v], rest[j][v]);
+          float u = COUPLED ? rest[j][v] * xr[j][v] : xr[j][v];
+          if (LOG && gr[j][v] > 0.f) f[j][v] = -f[j][v];
+          if (!all && n0 + j >= me.len) f[j][v] = 1.f, u = 0.f;
+          p[v] = compose(p[v], {gate_at(j, v), u});
+        }
       }
-    }
+#pragma unroll
+      for (int v = 0; v < V; ++v) q[v] = {p[v].a, 0.f};
+#pragma unroll
+      for (int j = L - 1; j >= 0; --j)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          q[v].s = gate_at(j, v) * (q[v].s + (!all && n0 + j >= me.len ? 0.f : yr[j][v]));
+    });
+    keep(xr);
+    keep(yr);
     auto& tot = totals[turn];
-    Pair q[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) q[v] = {p[v].a, 0.f};
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float e = !full && n0 + j >= me.len ? 0.f : yr[j][v];
-        q[v].s = gate_at(j, v) * (q[v].s + e);
-      }
     wave_scan<G::COLS, V, false>(p, hb);
     if ((tid & 63) >= 64 - G::COLS)
 #pragma unroll
@@ -498,25 +535,26 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, 
       for (int v = 0; v < V; ++v) tot[1][wave][cv + v] = q[v];
     __syncthreads();
     if (!CHAIN && tile > 0) load(tile - 1);
-    if (keeper) {
-      Pair own = tot[1][kWaves - 1][tid];
+    if (keeper) enter_waves<WIDTH, false>(start[turn][0], tot[0], h_start);
+    if constexpr (CHAIN) {
+      Pair own = {1.f, 0.f};
+      if (keeper)
 #pragma unroll
-      for (int i = kWaves - 2; i >= 0; --i) own = compose(own, tot[1][i][tid]);
-      float r = r_keep;
-      if constexpr (CHAIN) {
-        if (step == 0) own = {0.f, own.a * r + own.s};
-        const Pair b = chain_before(chain, step, last, mine, own);
-        if (step > 0) r = b.s;
-        r_keep = step == 0 ? own.s : own.a * r + own.s;
-      } else {
-        r_keep = own.a * r + own.s;
-      }
-      start[turn][1][tid] = r;
-      if (a.dh0 && tile == 0) a.dh0[mine] = r_keep;
+        for (int i = kWaves - 1; i >= 0; --i) own = compose(own, tot[1][i][tid]);
+      if (step == 0) own = {0.f, own.a * carried + own.s};
+      const Pair b = chain_before<WIDTH>(chain, step, last, group * WIDTH, own);
+      if (step > 0) carried = b.s;
     }
-    // h before each token needs nothing of the tiles behind.
+    if (keeper) {
+      carried = enter_waves<WIDTH, true>(start[turn][1], tot[1], carried);
+      if (a.dh0 && tile == 0) a.dh0[mine] = carried;
+    }
+    __syncthreads();
+    int drawn = 0;
+    if (CHAIN && tid == 0) drawn = draw();
     float h[V], hp[L][V];
-    enter<V, WIDTH, false>(h, start[turn][0], tot[0], cv, hb);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = hb[v].a * start[turn][0][wave][cv + v] + hb[v].s;
 #pragma unroll
     for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -524,31 +562,31 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, 
         hp[j][v] = h[v];
         h[v] = gate_at(j, v) * h[v] + (COUPLED ? rest[j][v] * xr[j][v] : xr[j][v]);
       }
-    __syncthreads();
-    int drawn = 0;
-    if (CHAIN && tid == 0) drawn = draw();
-    enter<V, WIDTH, true>(h, start[turn][1], tot[1], cv, rb);
-    T* to_dx = dx + (int64_t)(tile * kTile + L - 1) * a.xs.n;
-    T* to_dg = dg + (int64_t)(tile * kTile + L - 1) * a.gs.n;
-    const int stored = me.on ? a.N : 0;
+    keep(xr);
 #pragma unroll
-    for (int j = L - 1; j >= 0; --j, to_dx -= a.xs.n, to_dg -= a.gs.n) {
-      const bool dead = !full && n0 + j >= me.len;
-      float gx[V], gg[V];
+    for (int v = 0; v < V; ++v) h[v] = rb[v].a * start[turn][1][wave][cv + v] + rb[v].s;
+    when(full, [&](auto all) {
+      T* to_dx = dx + (int64_t)(tile * kTile + L - 1) * a.xs.n;
+      T* to_dg = dg + (int64_t)(tile * kTile + L - 1) * a.gs.n;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float dh = (dead ? 0.f : yr[j][v]) + h[v];
-        h[v] = gate_at(j, v) * dh;
-        gx[v] = COUPLED ? dh * rest[j][v] : dh;
-        gg[v] = dh * (COUPLED ? hp[j][v] - xr[j][v] : hp[j][v]);
-        gg[v] *= LOG ? (__float_as_uint(f[j][v]) >> 31 ? 0.f : f[j][v]) : f[j][v] * rest[j][v];
-        if (dead) gx[v] = gg[v] = 0.f;
+      for (int j = L - 1; j >= 0; --j, to_dx -= a.xs.n, to_dg -= a.gs.n) {
+        const bool dead = !all && n0 + j >= me.len;
+        float gx[V], gg[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float dh = (dead ? 0.f : yr[j][v]) + h[v];
+          h[v] = gate_at(j, v) * dh;
+          gx[v] = COUPLED ? dh * rest[j][v] : dh;
+          gg[v] = dh * (COUPLED ? hp[j][v] - xr[j][v] : hp[j][v]);
+          gg[v] *= LOG ? (__float_as_uint(f[j][v]) >> 31 ? 0.f : f[j][v]) : f[j][v] * rest[j][v];
+          if (dead) gx[v] = gg[v] = 0.f;
+        }
+        if (all || (me.on && n0 + j < a.N)) {
+          put<V>(to_dx, gx);
+          put<V>(to_dg, gg);
+        }
       }
-      if (n0 + j < stored) {
-        put<V>(to_dx, gx);
-        put<V>(to_dg, gg);
-      }
-    }
+    });
     ++step;
     if constexpr (CHAIN) {
       if (tid == 0) places[turn] = drawn;
@@ -588,9 +626,16 @@ hipError_t choose(int dtype, bool log_gate, bool coupled, F f) {
   return dtype == 1 ? flags(uint16_t()) : flags(float());
 }
 
-// Few columns: workgroups share the tiles of a column.
+// Chain form: from 5 tiles on, of fewer than 32768 columns.
+//  - Columns (bf16, 134 M elements, forward / backward, chain against loop):
+//    8192 columns 188 / 320 us against 371 / 558, 16384 174 / 283 against 208 / 314,
+//    32768 180 / 285 against 169 / 274: there the loop form's 512 workgroups fill
+//    the chip by themselves.
+//  - Tiles (32 columns, float32, a call on its own, chain against loop): 4 tiles
+//    13.8 / 15.2 us against 11.1 / 12.7, 5 tiles 13.4 / 14.9 against 11.4 / 15.4,
+//    8 tiles 13.4 / 14.8 against 14.7 / 23.5: the chain costs a second launch.
 bool chained(const ScanArgs& a) {
-  return a.ntiles > 1 && a.columns < 32768 && a.columns * a.ntiles <= INT32_MAX / 2;
+  return a.ntiles > 4 && a.columns < 32768 && a.columns * a.ntiles <= INT32_MAX / 2;
 }
 
 // Zeroes the counters and unsets the pairs of a chain in the workspace.
@@ -598,7 +643,8 @@ hipError_t start_chain(const ScanArgs& a, int groups, void* ws, Chain* c, hipStr
   c->words = (uint64_t*)ws;
   c->columns = a.columns;
   const long long n = chain_layout(a.ntiles, a.columns, groups, c->level);
-  scan_fill_kernel<<<dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(
+  const long long per = 2 * kThreads * kFillEach;
+  scan_fill_kernel<<<dim3((unsigned)((n + per - 1) / per)), dim3(kThreads), 0, s>>>(
       c->words, (long long)groups * kCounter, n);
   return hipGetLastError();
 }
