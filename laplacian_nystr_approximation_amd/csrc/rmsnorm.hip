@@ -7,7 +7,6 @@
 // way, the next row's already on their way while a row is worked on; each
 // workgroup takes every gridDim-th row and keeps its part of dw in registers, and
 // a second kernel adds the parts in a fixed order.  Both are bound by HBM.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "lapmix_internal.hpp"
@@ -87,14 +86,14 @@ struct Sum {
   __device__ float operator()(float a, float b) const { return a + b; }
 };
 struct Max {  // keeps NaN
-  __device__ float operator()(float a, float b) const { return b > a || b != b ? b : a; }
+  __device__ double operator()(double a, double b) const { return b > a || b != b ? b : a; }
 };
 
 // Over the lanes of a row (TPR of them, or with TPR = 0 the whole workgroup), in an
-// order fixed by the lanes; every lane gets the results.  `shared` has N floats for
+// order fixed by the lanes; every lane gets the results.  `shared` has N values for
 // each wave; a call may use it again after another barrier.
-template <int TPR, int N, typename F>
-__device__ __forceinline__ void over_row(float (&v)[N], float* shared, F f) {
+template <int TPR, int N, typename T, typename F>
+__device__ __forceinline__ void over_row(T (&v)[N], T* shared, F f) {
 #pragma unroll
   for (int m = 1; m < (TPR ? TPR : 64); m *= 2)
 #pragma unroll
@@ -113,9 +112,8 @@ __device__ __forceinline__ void over_row(float (&v)[N], float* shared, F f) {
   }
 }
 
-// The largest |y| that makes a scale is never below this: 448 times its
-// reciprocal stays finite.
-constexpr float kLeast = 0x1p-100f;
+// The largest |y| that makes a scale is never below this.
+constexpr double kLeast = 0x1p-100;
 
 // Where a lane works: TPR lanes to a row, or with TPR = 0 the whole workgroup.
 template <int TPR>
@@ -133,7 +131,10 @@ struct Place {
 template <typename X, typename R, typename Y, int V, int TPR, int CH>
 __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(NormArgs a) {
   constexpr bool Q = std::is_same<Y, E4M3>::value;
-  __shared__ float shared[2][kWide / 64];
+  __shared__ struct {
+    float f[kWide / 64];
+    double d[kWide / 64];
+  } shared;
   const Place<TPR> at;
   const long long row = (long long)blockIdx.x * at.rows + at.row;
   if (row >= a.rows) return;  // rows of part of a workgroup need no barrier
@@ -160,51 +161,59 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(Nor
       ss[0] += v[k][i] * v[k][i];
     }
   }
-  over_row<TPR>(ss, shared[0], Sum());
+  over_row<TPR>(ss, shared.f, Sum());
   const float rstd = 1.f / sqrtf(ss[0] / (float)a.C + a.eps);
-  float top[1] = {0.f};
+  // e4m3: the codes are those of 448 s w / max|s w|, from which the row's factor
+  // has cancelled, in 64 bits: there s w is exact, and no value comes to lie on the
+  // other side of a border between two codes.
+  double z[Q ? CH : 1][Q ? V : 1], top[1] = {0.};
+  auto scale_of = [&](double m) { return m * rstd < kLeast ? kLeast / 448. : m * rstd / 448.; };
+  auto factor_of = [&](double m) { return m * rstd < kLeast ? rstd * (448. / kLeast) : 448. / m; };
+  auto codes = [&](int k, int c, double factor) {
+    float q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = (float)(z[Q ? k : 0][Q ? i : 0] * factor);
+    put<Y, V>((Y*)a.y + row * a.C + c, q);
+  };
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = (k * at.lanes + at.lane) * V;
+    Raw<float, V> w;
     if (c < a.C) {
       if (a.s) put<R, V>((R*)a.s + row * a.C + c, v[k]);
-      const Raw<float, V> w = get<V>(a.w + c);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] *= rstd * w[i];
-      if constexpr (!Q) put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+      w = get<V>(a.w + c);
     }
     if constexpr (Q) {
-      float t = 0.f;
+      double t[1] = {0.};
 #pragma unroll
-      for (int i = 0; i < V; ++i) t = Max()(t, fabsf(v[k][i]));
+      for (int i = 0; i < V; ++i) {
+        z[k][i] = c < a.C ? (double)v[k][i] * (double)w[i] : 0.;
+        t[0] = Max()(t[0], fabs(z[k][i]));
+      }
       if (a.group) {
         // A group lies in neighbouring lanes of one wave, within a chunk.
-        for (int m = 1; m < a.group / V; m *= 2) t = Max()(t, __shfl_xor(t, m));
-        t = t < kLeast ? kLeast : t;
+        for (int m = 1; m < a.group / V; m *= 2) t[0] = Max()(t[0], __shfl_xor(t[0], m));
         if (c < a.C) {
-          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = t / 448.f;
-          const float inv = 448.f / t;
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[k][i] *= inv;
-          put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = (float)scale_of(t[0]);
+          codes(k, c, factor_of(t[0]));
         }
       }
-      top[0] = Max()(top[0], t);
+      top[0] = Max()(top[0], t[0]);
+    } else if (c < a.C) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] *= rstd * w[i];
+      put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
     }
   }
   if constexpr (Q) {
     if (a.group) return;
-    over_row<TPR>(top, shared[1], Max());
-    top[0] = top[0] < kLeast ? kLeast : top[0];
-    if (at.lane == 0) a.scale[row] = top[0] / 448.f;
-    const float inv = 448.f / top[0];
+    over_row<TPR>(top, shared.d, Max());
+    if (at.lane == 0) a.scale[row] = (float)scale_of(top[0]);
+    const double factor = factor_of(top[0]);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * at.lanes + at.lane) * V;
-      if (c >= a.C) continue;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] *= inv;
-      put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+      if (c < a.C) codes(k, c, factor);
     }
   }
 }
@@ -284,14 +293,30 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
     }
   }
   if (!a.dw) return;
-  // Rows that a workgroup takes side by side have a part each.
-  float* part = a.part + ((long long)blockIdx.x * at.rows + at.row) * a.C;
+  float* part = a.part + (long long)blockIdx.x * a.C;
+  if constexpr (TPR != 0) {
+    // The rows that the workgroup takes side by side make one part.
+    constexpr int ROWS = kNarrow / TPR;
+    __shared__ float sums[ROWS][TPR * CH * V];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int c = (k * at.lanes + at.lane) * V;
-    if (c < a.C)
+    for (int k = 0; k < CH; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) part[c + i] = dw[k][i];
+      for (int i = 0; i < V; ++i) sums[at.row][(k * TPR + at.lane) * V + i] = dw[k][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.C; c += kNarrow) {
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) sum += sums[r][c];
+      part[c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * at.lanes + at.lane) * V;
+      if (c < a.C)
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[c + i] = dw[k][i];
+    }
   }
 }
 
@@ -366,19 +391,21 @@ void with_types(const NormArgs& a, F f) {
 
 }  // namespace
 
-// Enough workgroups to fill the chip, and rows enough for each that the parts of
-// dw are small beside the rows.
+// Workgroups of the backward pass: about 16 waves to each of the 256 CUs, so that
+// the parts of dw stay small beside the rows, and four rows or more for each.  (16384
+// rows of 2560 bf16 columns, 5 waves a row: 114 us with 256 workgroups, 86 with 512,
+// 88 with 1024, 97 with 2048; 4096 rows of 1024, 2 waves: 21.7, 16.1, 14.6, 17.3.)
 static int norm_groups(long long rows, const Shape& shape) {
-  static const int G = getenv("LM_G") ? atoi(getenv("LM_G")) : 1024, D = getenv("LM_D") ? atoi(getenv("LM_D")) : 1;
-  const long long n = (rows + shape.rows() * D - 1) / (shape.rows() * D);
-  return (int)(n < G ? n : G);
+  const long long n = (rows + 4 * shape.rows() - 1) / (4 * shape.rows());
+  const int waves = shape.block / 64, most = waves > 4 ? 512 : 1024;
+  return (int)(n < most ? n : most);
 }
 
 size_t norm_part_count(const NormArgs& a) {
   size_t most = 0;
   for (bool vec : {false, true}) {
     const Shape shape = shape_of(a.C, vec);
-    const size_t n = (size_t)norm_groups(a.rows, shape) * shape.rows();
+    const size_t n = (size_t)norm_groups(a.rows, shape);
     most = n > most ? n : most;
   }
   return most;
@@ -400,7 +427,7 @@ hipError_t launch_norm_backward(const NormArgs& args, hipStream_t s) {
   NormArgs a = args;
   const Shape shape = shape_of(a.C, a.vec);
   const int groups = norm_groups(a.rows, shape);
-  a.parts = groups * shape.rows();
+  a.parts = groups;
   with_types(a, [&](auto x, auto r, auto y) {
     if constexpr (!std::is_same<decltype(y), E4M3>::value)
       with_shape(shape, [&](auto v, auto tpr, auto ch) {

@@ -170,18 +170,29 @@ __device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, ui
   return before;
 }
 
-// Forget gate f and 1 - f, each with a small relative error: one of them is
-// formed by a quotient (or exp, expm1), the other as 1 minus it only where it is
-// at least a half.
+// Forget gate f and 1 - f.  A gate close to 1 is passed on over many tokens, so it is
+// formed as 1 minus its complement: then its only error is the last rounding, which
+// has no drift, and the complement keeps its own relative accuracy.
 template <bool LOG>
 __device__ __forceinline__ void gate(float g, float& f, float& rest) {
   if constexpr (LOG) {
     g = g > 0.f ? 0.f : g;  // keeps NaN
-    f = __expf(g);
-    rest = g > -0.5f ? -expm1f(g) : 1.f - f;
+    const float e = __expf(g);
+    // exp(g) - 1 for g > -1/4 by its Taylor series: the first term left out is below
+    // 2^-24 of the sum.
+    float p = 1.f / 5040;
+    p = fmaf(p, g, 1.f / 720);
+    p = fmaf(p, g, 1.f / 120);
+    p = fmaf(p, g, 1.f / 24);
+    p = fmaf(p, g, 1.f / 6);
+    p = fmaf(p, g, 0.5f);
+    p = fmaf(p * g, g, g);
+    const bool near = g > -0.25f;
+    f = near ? 1.f + p : e;
+    rest = near ? -p : 1.f - e;
   } else {
     const float e = __expf(-fabsf(g));
-    const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    const float small = e * __builtin_amdgcn_rcpf(1.f + e), big = 1.f - small;
     f = g < 0.f ? small : big;
     rest = g < 0.f ? big : small;
   }
@@ -598,22 +609,29 @@ __global__ __launch_bounds__(kThreads, 2) void scan_backward_kernel(ScanArgs a, 
   }
 }
 
-template <typename T, bool LOG, bool COUPLED>
-__global__ __launch_bounds__(kThreads) void scan_step_kernel(StepArgs a) {
-  const long long col = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const int hd = a.H * a.d;
-  if (col >= (long long)a.B * hd) return;
-  const int b = (int)(col / hd), hc = (int)(col % hd);
+// One token: a wave takes 64 times V columns of one sequence, so the slot is the
+// same for all its lanes.  Bound by the launch, then by HBM (the states).
+template <typename T, bool VEC, bool LOG, bool COUPLED>
+__global__ __launch_bounds__(64) void scan_step_kernel(StepArgs a, int waves) {
+  constexpr int V = VEC ? 4 : 1;
+  const int b = blockIdx.x / waves, hd = a.H * a.d;
+  const int hc = ((blockIdx.x - b * waves) * 64 + threadIdx.x) * V;
   const int slot = a.slots ? a.slots[b] : b;
-  if (slot < 0 || slot >= a.n_slots) return;
-  const long long h = hc / a.d, c = hc % a.d;
-  float f, rest;
-  gate<LOG>(widen(((const T*)a.g)[b * a.gs.b + h * a.gs.h + c]), f, rest);
-  const float u = widen(((const T*)a.x)[b * a.xs.b + h * a.xs.h + c]);
-  const long long at = (long long)slot * hd + hc;
-  const float v = f * a.h_in[at] + (COUPLED ? rest * u : u);
-  a.h_out[at] = v;
-  narrow(v, (T*)a.y + b * a.ys.b + h * a.ys.h + c);
+  if (hc >= hd || slot < 0 || slot >= a.n_slots) return;
+  const int h = hc / a.d, c = hc - h * a.d;
+  const Raw<T, V> g = *(const Raw<T, V>*)((const T*)a.g + b * a.gs.b + h * a.gs.h + c);
+  const Raw<T, V> x = *(const Raw<T, V>*)((const T*)a.x + b * a.xs.b + h * a.xs.h + c);
+  const int64_t at = (int64_t)slot * hd + hc;
+  const Raw<float, V> from = *(const Raw<float, V>*)(a.h_in + at);
+  float to[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float f, rest;
+    gate<LOG>(g[v], f, rest);
+    to[v] = f * from[v] + (COUPLED ? rest * x[v] : x[v]);
+  }
+  put<V>(a.h_out + at, to);
+  put<V>((T*)a.y + b * a.ys.b + h * a.ys.h + c, to);
 }
 
 // Calls f with the storage type, gate and coupling as compile-time values.
@@ -697,10 +715,15 @@ hipError_t launch_scan_forward(const ScanArgs& a, void* ws, hipStream_t s) { ret
 hipError_t launch_scan_backward(const ScanArgs& a, void* ws, hipStream_t s) { return launch_scan<true>(a, ws, s); }
 
 hipError_t launch_scan_step(const StepArgs& a, hipStream_t s) {
-  const long long n = (long long)a.B * a.H * a.d;
   return choose(a.dtype, a.log_gate, a.coupled, [&](auto t, auto lg, auto cp) {
-    scan_step_kernel<decltype(t), decltype(lg)::value, decltype(cp)::value>
-        <<<dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(a);
+    using T = decltype(t);
+    constexpr bool LOG = decltype(lg)::value, COUPLED = decltype(cp)::value;
+    const int per = a.vec ? 256 : 64, waves = (a.H * a.d + per - 1) / per;
+    const dim3 grid((unsigned)a.B * (unsigned)waves), block(64);
+    if (a.vec)
+      scan_step_kernel<T, true, LOG, COUPLED><<<grid, block, 0, s>>>(a, waves);
+    else
+      scan_step_kernel<T, false, LOG, COUPLED><<<grid, block, 0, s>>>(a, waves);
     return hipGetLastError();
   });
 }

@@ -224,6 +224,40 @@ def test_scan_remembers_over_the_whole_sequence():
     c.check()
 
 
+@pytest.mark.parametrize("N", [5000, 70000, 700001])
+def test_scan_counts_exactly_over_long_sequences(N):
+    """Gates of 1 and 0 and whole inputs: states are counts since the last reset, exact in float32, and
+    so are the gradients; 700001 tokens take pairs of every level (4096 tiles are 524288 tokens)."""
+    torch = torch_mod()
+    d = 4
+    gen = torch.Generator().manual_seed(N)
+    for resets in (0, 97, 30011):
+        x = torch.randint(-2, 3, (1, 1, N, d), generator=gen).float().cuda()
+        dy = torch.randint(-2, 3, (1, 1, N, d), generator=gen).float().cuda()
+        c = Scan(1, 1, N, d, "f32", "log", state=False)
+        c.x, c.dy = x, dy
+        c.g = torch.zeros_like(x)
+        if resets:
+            c.g[:, :, resets::resets] = -float("inf")
+        c.forward()
+        c.backward()
+        torch.cuda.synchronize()
+        total = x.double().cumsum(2)
+        back = dy.double().flip(2).cumsum(2).flip(2)
+        if resets:
+            n = torch.arange(N, device="cuda")
+            first = n // resets * resets  # the run's first token
+            before = torch.where(first > 0, first - 1, 0)
+            total = total - torch.where(first[:, None] > 0, total[0, 0, before], 0.0)
+            after = first + resets  # the next run's
+            back = back - torch.where(after[:, None] < N, back[0, 0, after.clamp(max=N - 1)], 0.0)
+        assert torch.equal(c.y.double(), total) and torch.equal(c.hN.double(), total[:, :, -1])
+        assert torch.equal(c.dx.double(), back) and torch.equal(c.dh0.double()[0, 0], back[0, 0, 0])
+        hp = torch.cat([torch.zeros_like(total[:, :, :1]), total[:, :, :-1]], 2)
+        want = torch.where(c.g == 0, back * hp, torch.zeros_like(hp))
+        assert torch.equal(c.dg, want.float())
+
+
 def test_scan_nan_stays_in_its_column():
     torch = torch_mod()
     c = Scan(1, 2, 3000, 64, "f32")
@@ -539,6 +573,15 @@ class Norm:
         off = np.abs(q - v)
         assert np.all(off <= O.e4m3_half_step(np.abs(v) * (1 + 2 * U)) * (1 + 1e-9) + 2 * rel * np.abs(v))
         assert np.all(np.abs(q).reshape(R, C // G, G).max(2) <= 448)
+        # In groups that are not all tiny the norm's factor cancels: the codes are those of
+        # 448 s w / max|s w| in 64 bits (rounded to 32, then to e4m3), none on the other side of a border.
+        z = (s * w).reshape(R, C // G, G)
+        m = np.abs(z).max(2, keepdims=True)
+        ok = np.broadcast_to(np.abs(y).reshape(R, C // G, G).max(2, keepdims=True) > 2.0 ** -99, z.shape)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            want = np.where(ok, z * (448.0 / m), 0.0)
+        want = _np(torch.from_numpy(want.astype(np.float32)).to(torch.float8_e4m3fn))
+        assert np.array_equal(q.reshape(z.shape)[ok], want[ok])
 
     def check_backward(self):
         torch_mod().cuda.synchronize()
