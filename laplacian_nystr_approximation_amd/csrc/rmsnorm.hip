@@ -47,46 +47,35 @@ __device__ __forceinline__ Raw<T, V> get(const T* p) {
   return *(const Raw<T, V>*)p;
 }
 
-struct E4M3 {
-  uint8_t code;
-};
+struct E4M3 {};
+
+// V floats rounded to T.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> pack(const float* v) {
+  Raw<T, V> r;
+  if constexpr (V == 1) {
+    narrow(v[0], &r.e);
+  } else if constexpr (sizeof(T) == 4) {
+    r.lo = (f32x4){v[0], v[1], v[2], v[3]};
+    r.hi = (f32x4){v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.e[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, lapnys::bf16x2));
+  }
+  return r;
+}
 
 template <typename T, int V>
 __device__ __forceinline__ void put(T* p, const float* v) {
-  if constexpr (std::is_same<T, E4M3>::value) {
-    if constexpr (V == 1) {
-      p->code = (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false) & 0xff);
-    } else {
-      int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-      a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
-      b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
-      *(int2*)p = make_int2(a, b);
-    }
-  } else if constexpr (V == 1) {
-    narrow(v[0], p);
-  } else if constexpr (sizeof(T) == 4) {
-    *(f32x4*)p = (f32x4){v[0], v[1], v[2], v[3]};
-    *(f32x4*)(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
-  } else {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){v[2 * i], v[2 * i + 1]}, lapnys::bf16x2));
-    *(u32x4*)p = o;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ float rounded(float v) {
-  return sizeof(T) == 4 ? v : (float)(__bf16)v;
+  *(Raw<T, V>*)p = pack<T, V>(v);
 }
 
 struct Sum {
   __device__ float operator()(float a, float b) const { return a + b; }
 };
-struct Max {  // keeps NaN
-  __device__ double operator()(double a, double b) const { return b > a || b != b ? b : a; }
+struct Max {  // of what is not NaN
+  __device__ double operator()(double a, double b) const { return fmax(a, b); }
 };
 
 // Over the lanes of a row (TPR of them, or with TPR = 0 the whole workgroup), in an
@@ -112,8 +101,90 @@ __device__ __forceinline__ void over_row(T (&v)[N], T* shared, F f) {
   }
 }
 
+// e4m3: the codes are those of 448 s w / max|s w|, from which the row's factor has
+// cancelled, decided in 64 bits, where s w is exact: no value comes to lie on the
+// other side of a border between two codes.  Nearly always 32 bits tell as much.
+
 // The largest |y| that makes a scale is never below this.
 constexpr double kLeast = 0x1p-100;
+
+__device__ __forceinline__ float scale_of(double m, float rstd) {
+  const double top = m * rstd;
+  return (float)((top < kLeast ? kLeast : top) * (1. / 448.));
+}
+
+// Products of 32 bits in this range, and their remainders, neither overflow nor lose bits.
+__device__ __forceinline__ bool ordinary(float z) { return z > 0x1p-90f && z < 0x1p100f; }
+
+// The largest |s w| of a lane, exactly: the largest product rounded to 32 bits, and
+// what rounding took from the products that come to it.
+template <int V>
+__device__ __forceinline__ double largest(const float (&s)[V], const Raw<float, V>& w) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(s[i] * w[i]));
+  double t = 0.;
+  if (ordinary(m)) {
+    float rest = -m;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float r = fmaf(fabsf(s[i]), fabsf(w[i]), -m);
+      rest = fabsf(s[i] * w[i]) == m ? fmaxf(rest, r) : rest;
+    }
+    t = (double)m + (double)rest;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) t = fmax(t, fabs((double)s[i] * (double)w[i]));
+  }
+  return t;
+}
+
+// Four codes, the first in the lowest byte.
+__device__ __forceinline__ int codes4(float a, float b, float c, float d) {
+  return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
+// The codes by 32 bits (m: the largest |s w|, rounded); false if they are not certain.
+template <int V>
+__device__ __forceinline__ bool codes_of(int (&code)[2], const float (&s)[V], const Raw<float, V>& w, float m, float rstd) {
+  // 32 bits are off by at most seven roundings, less than 2^-21 of the value: where a
+  // little less and a little more than it have the same code, that is the code.
+  const float near = __builtin_amdgcn_rcpf(m) * 448.f;
+  const float less = near * (1.f - 0x1p-20f), more = near * (1.f + 0x1p-20f);
+  auto four = [&](int i, float f) {
+    if constexpr (V == 8)
+      return codes4(s[i] * w[i] * f, s[i + 1] * w[i + 1] * f, s[i + 2] * w[i + 2] * f, s[i + 3] * w[i + 3] * f);
+    else
+      return codes4(s[0] * w[0] * f, 0.f, 0.f, 0.f);
+  };
+  bool sure = ordinary(m) && m * rstd > 2 * (float)kLeast;
+#pragma unroll
+  for (int k = 0; k < (V == 8 ? 2 : 1); ++k) {
+    code[k] = four(4 * k, less);
+    sure = sure && code[k] == four(4 * k, more);
+  }
+  return sure;
+}
+
+// The codes by 64 bits.
+template <int V>
+__device__ __forceinline__ void exact_codes(int (&code)[2], const float (&s)[V], const Raw<float, V>& w, double m,
+                                            float rstd) {
+  const double factor = m * rstd < kLeast ? rstd * (448. / kLeast) : 448. / m;
+  float q[8] = {};
+#pragma unroll
+  for (int i = 0; i < V; ++i) q[i] = (float)((double)s[i] * (double)w[i] * factor);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) code[k] = codes4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
+}
+
+template <int V>
+__device__ __forceinline__ void put_codes(uint8_t* p, const int (&code)[2]) {
+  if constexpr (V == 8)
+    *(int2*)p = make_int2(code[0], code[1]);
+  else
+    *p = (uint8_t)code[0];
+}
 
 // Where a lane works: TPR lanes to a row, or with TPR = 0 the whole workgroup.
 template <int TPR>
@@ -154,66 +225,68 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(Nor
   float v[CH][V], ss[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const bool on = (k * at.lanes + at.lane) * V < a.C;
+    const int c = (k * at.lanes + at.lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[k][i] = c < a.C ? (a.r ? xr[k][i] + rr[k][i] : xr[k][i]) : 0.f;
+    rr[k] = pack<R, V>(v[k]);
+    if (c < a.C && a.s) *(Raw<R, V>*)((R*)a.s + row * a.C + c) = rr[k];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[k][i] = on ? rounded<R>(a.r ? xr[k][i] + rr[k][i] : xr[k][i]) : 0.f;
+      v[k][i] = rr[k][i];
       ss[0] += v[k][i] * v[k][i];
     }
   }
   over_row<TPR>(ss, shared.f, Sum());
   const float rstd = 1.f / sqrtf(ss[0] / (float)a.C + a.eps);
-  // e4m3: the codes are those of 448 s w / max|s w|, from which the row's factor
-  // has cancelled, in 64 bits: there s w is exact, and no value comes to lie on the
-  // other side of a border between two codes.
-  double z[Q ? CH : 1][Q ? V : 1], top[1] = {0.};
-  auto scale_of = [&](double m) { return m * rstd < kLeast ? kLeast / 448. : m * rstd / 448.; };
-  auto factor_of = [&](double m) { return m * rstd < kLeast ? rstd * (448. / kLeast) : 448. / m; };
-  auto codes = [&](int k, int c, double factor) {
-    float q[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = (float)(z[Q ? k : 0][Q ? i : 0] * factor);
-    put<Y, V>((Y*)a.y + row * a.C + c, q);
-  };
+  Raw<float, V> w[CH];
+  double top[1] = {0.};
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = (k * at.lanes + at.lane) * V;
-    Raw<float, V> w;
     if (c < a.C) {
-      if (a.s) put<R, V>((R*)a.s + row * a.C + c, v[k]);
-      w = get<V>(a.w + c);
+      w[k] = get<V>(a.w + c);
+      if constexpr (!Q) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] *= rstd * w[k][i];
+        put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+      }
     }
     if constexpr (Q) {
-      double t[1] = {0.};
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        z[k][i] = c < a.C ? (double)v[k][i] * (double)w[i] : 0.;
-        t[0] = Max()(t[0], fabs(z[k][i]));
-      }
       if (a.group) {
         // A group lies in neighbouring lanes of one wave, within a chunk.
-        for (int m = 1; m < a.group / V; m *= 2) t[0] = Max()(t[0], __shfl_xor(t[0], m));
-        if (c < a.C) {
-          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = (float)scale_of(t[0]);
-          codes(k, c, factor_of(t[0]));
-        }
-      }
-      top[0] = Max()(top[0], t[0]);
-    } else if (c < a.C) {
+        float m = 0.f;
+        if (c < a.C)
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] *= rstd * w[i];
-      put<Y, V>((Y*)a.y + row * a.C + c, v[k]);
+          for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(v[k][i] * w[k][i]));
+        for (int o = 1; o < a.group / V; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
+        int code[2];
+        const bool sure = c >= a.C || codes_of<V>(code, v[k], w[k], m, rstd);
+        double exact = m;
+        if (!__all(sure)) {
+          exact = c < a.C ? largest<V>(v[k], w[k]) : 0.;
+          for (int o = 1; o < a.group / V; o *= 2) exact = fmax(exact, __shfl_xor(exact, o));
+          if (!sure) exact_codes<V>(code, v[k], w[k], exact, rstd);
+        }
+        if (c < a.C) {
+          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = scale_of(exact, rstd);
+          put_codes<V>((uint8_t*)a.y + row * a.C + c, code);
+        }
+      } else if (c < a.C) {
+        top[0] = fmax(top[0], largest<V>(v[k], w[k]));
+      }
     }
   }
   if constexpr (Q) {
     if (a.group) return;
     over_row<TPR>(top, shared.d, Max());
-    if (at.lane == 0) a.scale[row] = (float)scale_of(top[0]);
-    const double factor = factor_of(top[0]);
+    if (at.lane == 0) a.scale[row] = scale_of(top[0], rstd);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * at.lanes + at.lane) * V;
-      if (c < a.C) codes(k, c, factor);
+      int code[2];
+      if (c >= a.C) continue;
+      if (!codes_of<V>(code, v[k], w[k], (float)top[0], rstd)) exact_codes<V>(code, v[k], w[k], top[0], rstd);
+      put_codes<V>((uint8_t*)a.y + row * a.C + c, code);
     }
   }
 }
