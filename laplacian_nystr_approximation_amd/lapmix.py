@@ -85,23 +85,29 @@ def make_norm_params(*, B, H, N, d, x_dtype="f32", r_dtype="f32", y_dtype="f32",
                               _NAMES.get(y_dtype, y_dtype), group, eps, 0)
 
 
-# Decoding steps are a few microseconds long on the GPU, so these checks go by the
-# shortest ways to a tensor's facts.
-def _stream(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return _given_stream(stream)
+# Decoding steps are a few microseconds long on the GPU, so the checks of a call go by
+# the shortest ways to a tensor's facts and ask for the current device once (``dev``).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _device_ptr(t):
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be device tensors (got a tensor on the host)")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _current():
+    """Index of the current device; without a GPU, where every tensor is refused as a host tensor, -1."""
+    return torch.cuda.current_device() if _raw_stream and torch.cuda.device_count() else -1
+
+
+def _stream(stream, dev):
+    return _raw_stream(dev) if stream is None and dev >= 0 else _given_stream(stream)
+
+
+def _device_ptr(t, dev):
+    if t.get_device() != dev or not t.is_cuda:
+        if not t.is_cuda:
+            raise ValueError("tensor arguments must be device tensors (got a tensor on the host)")
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return t.data_ptr()
 
 
-def _flat(name, t, size, count):
+def _flat(name, t, size, count, dev):
     """Pointer of a dense tensor argument that holds at least ``count`` elements of ``size`` bytes."""
     if t is None or isinstance(t, int):
         return t
@@ -110,24 +116,23 @@ def _flat(name, t, size, count):
                          f"got {t.numel()} of {t.element_size()}")
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
-    return _device_ptr(t)
+    return _device_ptr(t, dev)
 
 
-def _heads(name, t, size, p):
+def _heads(name, t, size, shape, dev):
     """(pointer, strides) of a [B, H, N, d] tensor argument; strides None for a raw pointer."""
     if t is None or isinstance(t, int):
         return t, None
-    B, H, N, d = p.B, p.H, p.N, p.d
-    if t.element_size() != size or t.shape != (B, H, N, d):
-        raise ValueError(f"{name}: expected [{B}, {H}, {N}, {d}] of {size} bytes, "
-                         f"got {list(t.shape)} of {t.element_size()}")
-    ptr = _device_ptr(t)
+    if t.element_size() != size or t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)} of {size} bytes, got {list(t.shape)} of {t.element_size()}")
+    ptr = _device_ptr(t, dev)
     b, h, n, c = t.stride()
+    B, H, N, d = shape
     if c != 1 and d != 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {c})")
     # Strides of dimensions of size 1 do not matter; all zero would mean a dense tensor.
     st = (b if B > 1 else 0, h if H > 1 else 0, n if N > 1 else 0)
-    if not (b or h or n) and B * H * N > 1:
+    if st == (0, 0, 0) and B * H * N > 1:
         raise ValueError(f"{name}: one row repeated for every token is not supported")
     return ptr, st
 
@@ -149,6 +154,22 @@ def lapmix_scan_states_size(params: lapmix_scan_params) -> int:
     return n.value
 
 
+def _tiles(N):
+    return -(-N // LAPMIX_SCAN_TILE)
+
+
+def _scan_shape(p):
+    """[B, H, N, d], element size and columns of a recurrence, and the current device."""
+    B, H, N, d = p.B, p.H, p.N, p.d
+    return (B, H, N, d), _SIZES.get(p.dtype, 0), B * H * d, _current()
+
+
+def _norm_shape(p):
+    """[B, H, N, d], row width, elements and the stream's element size of a norm, and the current device."""
+    B, H, N, d = p.B, p.H, p.N, p.d
+    return (B, H, N, d), H * d, B * N * H * d, _SIZES.get(p.r_dtype, 0), _current()
+
+
 def _scan_params(params, xs, gs, ys):
     p = lapmix_scan_params.from_buffer_copy(params)
     if xs is not None:
@@ -163,53 +184,51 @@ def _scan_params(params, xs, gs, ys):
 def lapmix_scan_forward_ws(x, g, y, params: lapmix_scan_params, ws, h0=None, hN=None, states=None, lengths=None,
                            stream=None) -> None:
     """y (and the last state hN, and the states that the backward reads) of h_t = f_t h_{t-1} + i_t x_t."""
-    size = _SIZES.get(params.dtype, 0)
-    cols = params.B * params.H * params.d
-    xp, xs = _heads("x", x, size, params)
-    gp, gs = _heads("g", g, size, params)
-    yp, ys = _heads("y", y, size, params)
+    shape, size, cols, dev = _scan_shape(params)
+    xp, xs = _heads("x", x, size, shape, dev)
+    gp, gs = _heads("g", g, size, shape, dev)
+    yp, ys = _heads("y", y, size, shape, dev)
     wp, wn = _ws(ws)
     _check(_lib.lapmix_scan_forward_ws(
-        xp, gp, _flat("h0", h0, 4, cols), _flat("lengths", lengths, 4, params.B), yp, _flat("hN", hN, 4, cols),
-        _flat("states", states, 4, cols * (-(-params.N // LAPMIX_SCAN_TILE))), _scan_params(params, xs, gs, ys), wp, wn,
-        _stream(stream)), "lapmix_scan_forward_ws")
+        xp, gp, _flat("h0", h0, 4, cols, dev), _flat("lengths", lengths, 4, shape[0], dev), yp,
+        _flat("hN", hN, 4, cols, dev), _flat("states", states, 4, cols * _tiles(shape[2]), dev),
+        _scan_params(params, xs, gs, ys), wp, wn, _stream(stream, dev)), "lapmix_scan_forward_ws")
 
 
 def lapmix_scan_backward_ws(x, g, states, dy, dx, dg, params: lapmix_scan_params, ws, dhN=None, dh0=None,
                             lengths=None, stream=None) -> None:
     """Gradients of sum(dy * y) + sum(dhN * hN) into dx, dg and dh0; dx and dg have the strides of x and g."""
-    size = _SIZES.get(params.dtype, 0)
-    cols = params.B * params.H * params.d
-    xp, xs = _heads("x", x, size, params)
-    gp, gs = _heads("g", g, size, params)
-    dyp, ys = _heads("dy", dy, size, params)
-    dxp, dxs = _heads("dx", dx, size, params)
-    dgp, dgs = _heads("dg", dg, size, params)
+    shape, size, cols, dev = _scan_shape(params)
+    xp, xs = _heads("x", x, size, shape, dev)
+    gp, gs = _heads("g", g, size, shape, dev)
+    dyp, ys = _heads("dy", dy, size, shape, dev)
+    dxp, dxs = _heads("dx", dx, size, shape, dev)
+    dgp, dgs = _heads("dg", dg, size, shape, dev)
     _agree("dx", dxs, "x", xs)
     _agree("dg", dgs, "g", gs)
     wp, wn = _ws(ws)
     _check(_lib.lapmix_scan_backward_ws(
-        xp, gp, _flat("states", states, 4, cols * (-(-params.N // LAPMIX_SCAN_TILE))),
-        _flat("lengths", lengths, 4, params.B), dyp, _flat("dhN", dhN, 4, cols), dxp, dgp,
-        _flat("dh0", dh0, 4, cols), _scan_params(params, xs, gs, ys), wp, wn, _stream(stream)),
-        "lapmix_scan_backward_ws")
+        xp, gp, _flat("states", states, 4, cols * _tiles(shape[2]), dev), _flat("lengths", lengths, 4, shape[0], dev),
+        dyp, _flat("dhN", dhN, 4, cols, dev), dxp, dgp, _flat("dh0", dh0, 4, cols, dev),
+        _scan_params(params, xs, gs, ys), wp, wn, _stream(stream, dev)), "lapmix_scan_backward_ws")
 
 
 def lapmix_scan_step(x, g, y, h_in, h_out, params: lapmix_scan_params, slots=None, n_slots=None, stream=None) -> None:
     """One token for every sequence: y = h_out[slot] = f h_in[slot] + i x.  ``h_in`` and ``h_out`` are
     float32 [n_slots, H, d] pools (``n_slots`` is taken from h_in's shape unless given)."""
-    size = _SIZES.get(params.dtype, 0)
     if n_slots is None:
         if isinstance(h_in, int):
             raise ValueError("n_slots is needed with a raw pool pointer")
         n_slots = h_in.shape[0]
-    cols = n_slots * params.H * params.d
-    xp, xs = _heads("x", x, size, params)
-    gp, gs = _heads("g", g, size, params)
-    yp, ys = _heads("y", y, size, params)
+    shape, size, _, dev = _scan_shape(params)
+    pool = n_slots * shape[1] * shape[3]
+    xp, xs = _heads("x", x, size, shape, dev)
+    gp, gs = _heads("g", g, size, shape, dev)
+    yp, ys = _heads("y", y, size, shape, dev)
     _check(_lib.lapmix_scan_step(
-        xp, gp, _flat("slots", slots, 4, params.B), _flat("h_in", h_in, 4, cols), _flat("h_out", h_out, 4, cols),
-        n_slots, yp, _scan_params(params, xs, gs, ys), _stream(stream)), "lapmix_scan_step")
+        xp, gp, _flat("slots", slots, 4, shape[0], dev), _flat("h_in", h_in, 4, pool, dev),
+        _flat("h_out", h_out, 4, pool, dev), n_slots, yp, _scan_params(params, xs, gs, ys), _stream(stream, dev)),
+        "lapmix_scan_step")
 
 
 def _norm_params(params, xs):
@@ -223,13 +242,12 @@ def _norm_params(params, xs):
 def lapmix_norm_forward(x, w, y, params: lapmix_norm_params, r=None, s=None, scale=None, stream=None) -> None:
     """s = x + r and y = s / sqrt(mean(s^2) + eps) * w for every token's row (e4m3: with ``scale``)."""
     p = params
-    C = p.H * p.d
-    n = p.B * p.N * C
-    rs, ysz = _SIZES.get(p.r_dtype, 0), _SIZES.get(p.y_dtype, 0)
-    xp, xs = _heads("x", x, _SIZES.get(p.x_dtype, 0), p)
+    shape, C, n, rs, dev = _norm_shape(p)
+    xp, xs = _heads("x", x, _SIZES.get(p.x_dtype, 0), shape, dev)
     _check(_lib.lapmix_norm_forward(
-        xp, _flat("r", r, rs, n), _flat("w", w, 4, C), _flat("s", s, rs, n), _flat("y", y, ysz, n),
-        _flat("scale", scale, 4, n // (p.group or C)), _norm_params(p, xs), _stream(stream)), "lapmix_norm_forward")
+        xp, _flat("r", r, rs, n, dev), _flat("w", w, 4, C, dev), _flat("s", s, rs, n, dev),
+        _flat("y", y, _SIZES.get(p.y_dtype, 0), n, dev), _flat("scale", scale, 4, n // max(p.group or C, 1), dev),
+        _norm_params(p, xs), _stream(stream, dev)), "lapmix_norm_forward")
 
 
 def lapmix_norm_workspace_size(params: lapmix_norm_params) -> int:
@@ -242,12 +260,10 @@ def lapmix_norm_backward_ws(dy, s, w, params: lapmix_norm_params, ws, ds=None, d
                             stream=None) -> None:
     """Gradients of sum(dy * y) + sum(ds * s) into dr (the stream's), dx (the branch's) and dw."""
     p = params
-    C = p.H * p.d
-    n = p.B * p.N * C
-    rs = _SIZES.get(p.r_dtype, 0)
-    dxp, xs = _heads("dx", dx, _SIZES.get(p.x_dtype, 0), p)
+    shape, C, n, rs, dev = _norm_shape(p)
+    dxp, xs = _heads("dx", dx, _SIZES.get(p.x_dtype, 0), shape, dev)
     wp, wn = _ws(ws)
     _check(_lib.lapmix_norm_backward_ws(
-        _flat("dy", dy, _SIZES.get(p.y_dtype, 0), n), _flat("s", s, rs, n), _flat("w", w, 4, C),
-        _flat("ds", ds, rs, n), _flat("dr", dr, rs, n), dxp, _flat("dw", dw, 4, C), _norm_params(p, xs), wp, wn,
-        _stream(stream)), "lapmix_norm_backward_ws")
+        _flat("dy", dy, _SIZES.get(p.y_dtype, 0), n, dev), _flat("s", s, rs, n, dev), _flat("w", w, 4, C, dev),
+        _flat("ds", ds, rs, n, dev), _flat("dr", dr, rs, n, dev), dxp, _flat("dw", dw, 4, C, dev), _norm_params(p, xs),
+        wp, wn, _stream(stream, dev)), "lapmix_norm_backward_ws")
