@@ -70,7 +70,8 @@ enum { LAPMIX_GATE_LOG = 1u, LAPMIX_COUPLED = 2u };
 #define LAPMIX_SCAN_TILE 128
 
 typedef struct {
-  int32_t B, H, N, d;   /* batches, heads, tokens, channels */
+  int32_t B, H, N, d;   /* batches, heads, tokens (up to 2^30), channels
+                           (B * H * d up to 2^28; beyond: LAPNYS_ERR_UNSUPPORTED) */
   int32_t dtype;        /* lapnys_dtype of x, g, y, dy, dx and dg */
   uint32_t flags;       /* LAPMIX_GATE_LOG | LAPMIX_COUPLED, or 0 */
   int64_t x_stride[3];  /* of x and dx: batch, head, token, in elements */

@@ -134,6 +134,9 @@ int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- recurrence
 
+constexpr int64_t kMaxScanColumns = (int64_t)1 << 28;
+constexpr int32_t kMaxScanTokens = 1 << 30;
+
 int scan_plan(const lapmix_scan_params* p, lapmix::ScanArgs* a) {
   *a = {};
   if (!p) return LAPNYS_ERR_INVALID_ARG;
@@ -144,8 +147,10 @@ int scan_plan(const lapmix_scan_params* p, lapmix::ScanArgs* a) {
       !take_strides(p->y_stride, p->B, p->H, p->N, p->d, &a->ys))
     return LAPNYS_ERR_INVALID_ARG;
   if (!storage_type(p->dtype)) return LAPNYS_ERR_UNSUPPORTED;
-  // Columns and tiles are counted in 32 bits, elements in 64.
-  if ((int64_t)p->B * p->H > INT32_MAX || (int64_t)p->B * p->H * p->d > INT32_MAX) return LAPNYS_ERR_UNSUPPORTED;
+  // Tokens and columns are counted in 32 bits, a launch's lanes too, elements in 64.
+  if ((int64_t)p->B * p->H > kMaxScanColumns || (int64_t)p->B * p->H * p->d > kMaxScanColumns ||
+      p->N > kMaxScanTokens)
+    return LAPNYS_ERR_UNSUPPORTED;
   a->B = p->B, a->H = p->H, a->N = p->N, a->d = p->d;
   a->dtype = p->dtype;
   a->columns = (long long)p->B * p->H * p->d;
@@ -230,6 +235,8 @@ int scan_step(const void* x, const void* g, const int32_t* slots, const float* h
   if (p->N != 1) return LAPNYS_ERR_SHAPE;
   if (!x || !g || !h_in || !h_out || !y || n_slots <= 0) return LAPNYS_ERR_INVALID_ARG;
   if (!slots && n_slots < p->B) return LAPNYS_ERR_SHAPE;
+  // A wave takes columns of one sequence: as many sequences as a launch has waves.
+  if ((int64_t)p->B * (((int64_t)p->H * p->d + 63) / 64) > (1 << 25)) return LAPNYS_ERR_UNSUPPORTED;
   const int64_t e = element_size(a.dtype), pool = (int64_t)n_slots * a.H * a.d;
   const View vx = strided_view(x, a.B, a.H, 1, a.d, a.xs, e), vg = strided_view(g, a.B, a.H, 1, a.d, a.gs, e),
              vy = strided_view(y, a.B, a.H, 1, a.d, a.ys, e), vin = dense_view(h_in, pool, 4),

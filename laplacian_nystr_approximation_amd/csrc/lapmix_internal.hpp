@@ -65,6 +65,7 @@ hipError_t launch_scan_step(const StepArgs& a, hipStream_t s);
 struct NormArgs {
   int H, N, d, C;
   long long rows;    // B * N
+  long long first;   // the launch's first row (forward)
   int x_dtype, r_dtype, y_dtype, group;
   float eps;
   bool vec;

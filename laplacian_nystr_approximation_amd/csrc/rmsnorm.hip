@@ -207,7 +207,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(Nor
     double d[kWide / 64];
   } shared;
   const Place<TPR> at;
-  const long long row = (long long)blockIdx.x * at.rows + at.row;
+  const long long row = a.first + (long long)blockIdx.x * at.rows + at.row;
   if (row >= a.rows) return;  // rows of part of a workgroup need no barrier
   const uint32_t b = (uint32_t)row / (uint32_t)a.N, n = (uint32_t)row % (uint32_t)a.N;
   const X* x = (const X*)a.x + b * a.xs.b + n * a.xs.n;
@@ -487,16 +487,24 @@ size_t norm_part_count(const NormArgs& a) {
   return most;
 }
 
-hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
+hipError_t launch_norm_forward(const NormArgs& args, hipStream_t s) {
+  NormArgs a = args;
   const Shape shape = shape_of(a.C, a.vec);
-  const dim3 grid((unsigned)((a.rows + shape.rows() - 1) / shape.rows())), block(shape.block);
-  with_types(a, [&](auto x, auto r, auto y) {
-    with_shape(shape, [&](auto v, auto tpr, auto ch) {
-      norm_forward_kernel<decltype(x), decltype(r), decltype(y), decltype(v)::value, decltype(tpr)::value,
-                          decltype(ch)::value><<<grid, block, 0, s>>>(a);
+  // A launch has at most 2^32 - 1 lanes: many rows go in several.
+  const long long most = ((long long)1 << 31) / shape.block;
+  hipError_t e = hipSuccess;
+  for (a.first = 0; a.first < a.rows && e == hipSuccess; a.first += most * shape.rows()) {
+    const long long groups = (a.rows - a.first + shape.rows() - 1) / shape.rows();
+    const dim3 grid((unsigned)(groups < most ? groups : most)), block(shape.block);
+    with_types(a, [&](auto x, auto r, auto y) {
+      with_shape(shape, [&](auto v, auto tpr, auto ch) {
+        norm_forward_kernel<decltype(x), decltype(r), decltype(y), decltype(v)::value, decltype(tpr)::value,
+                            decltype(ch)::value><<<grid, block, 0, s>>>(a);
+      });
     });
-  });
-  return hipGetLastError();
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 hipError_t launch_norm_backward(const NormArgs& args, hipStream_t s) {

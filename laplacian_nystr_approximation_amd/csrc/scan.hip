@@ -81,7 +81,7 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* at) {
 // matters if a workspace is written from outside while the kernel runs: the
 // results are then NaN.
 __device__ __forceinline__ Pair wait_for(const uint64_t* at, uint64_t w) {
-  for (int tries = 0; (uint32_t)w == (uint32_t)kUnset && tries < (1 << 20); ++tries) {
+  for (int tries = 0; (uint32_t)w == (uint32_t)kUnset && tries < (1 << 18); ++tries) {
     __builtin_amdgcn_s_sleep(1);
     w = peek(at);
   }

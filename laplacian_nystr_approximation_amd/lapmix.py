@@ -24,6 +24,10 @@ LAPMIX_COUPLED = 2
 LAPMIX_SCAN_TILE = 128
 
 _SIZES = {LAPNYS_F32: 4, LAPNYS_BF16: 2, LAPMIX_E4M3: 1}
+_INDEX = (torch.int32,)
+# Tensor types by element size: the storage types, or their bit patterns.
+_TYPES = {4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16),
+          1: (torch.float8_e4m3fn, torch.uint8, torch.int8)}
 _NAMES = {"f32": LAPNYS_F32, "bf16": LAPNYS_BF16, "e4m3": LAPMIX_E4M3}
 _stride = ctypes.c_int64 * 3
 
@@ -107,13 +111,13 @@ def _device_ptr(t, dev):
     return t.data_ptr()
 
 
-def _flat(name, t, size, count, dev):
+def _flat(name, t, size, count, dev, types=None):
     """Pointer of a dense tensor argument that holds at least ``count`` elements of ``size`` bytes."""
     if t is None or isinstance(t, int):
         return t
-    if t.element_size() != size or t.numel() < count:
+    if t.dtype not in (types or _TYPES.get(size, ())) or t.numel() < count:
         raise ValueError(f"{name}: expected at least {count} elements of {size} bytes, "
-                         f"got {t.numel()} of {t.element_size()}")
+                         f"got {t.numel()} of {t.element_size()} ({t.dtype})")
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
     return _device_ptr(t, dev)
@@ -123,8 +127,9 @@ def _heads(name, t, size, shape, dev):
     """(pointer, strides) of a [B, H, N, d] tensor argument; strides None for a raw pointer."""
     if t is None or isinstance(t, int):
         return t, None
-    if t.element_size() != size or t.shape != shape:
-        raise ValueError(f"{name}: expected {list(shape)} of {size} bytes, got {list(t.shape)} of {t.element_size()}")
+    if t.dtype not in _TYPES.get(size, ()) or t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)} of {size} bytes, "
+                         f"got {list(t.shape)} of {t.element_size()} ({t.dtype})")
     ptr = _device_ptr(t, dev)
     b, h, n, c = t.stride()
     B, H, N, d = shape
@@ -190,7 +195,7 @@ def lapmix_scan_forward_ws(x, g, y, params: lapmix_scan_params, ws, h0=None, hN=
     yp, ys = _heads("y", y, size, shape, dev)
     wp, wn = _ws(ws)
     _check(_lib.lapmix_scan_forward_ws(
-        xp, gp, _flat("h0", h0, 4, cols, dev), _flat("lengths", lengths, 4, shape[0], dev), yp,
+        xp, gp, _flat("h0", h0, 4, cols, dev), _flat("lengths", lengths, 4, shape[0], dev, _INDEX), yp,
         _flat("hN", hN, 4, cols, dev), _flat("states", states, 4, cols * _tiles(shape[2]), dev),
         _scan_params(params, xs, gs, ys), wp, wn, _stream(stream, dev)), "lapmix_scan_forward_ws")
 
@@ -208,8 +213,9 @@ def lapmix_scan_backward_ws(x, g, states, dy, dx, dg, params: lapmix_scan_params
     _agree("dg", dgs, "g", gs)
     wp, wn = _ws(ws)
     _check(_lib.lapmix_scan_backward_ws(
-        xp, gp, _flat("states", states, 4, cols * _tiles(shape[2]), dev), _flat("lengths", lengths, 4, shape[0], dev),
-        dyp, _flat("dhN", dhN, 4, cols, dev), dxp, dgp, _flat("dh0", dh0, 4, cols, dev),
+        xp, gp, _flat("states", states, 4, cols * _tiles(shape[2]), dev),
+        _flat("lengths", lengths, 4, shape[0], dev, _INDEX), dyp, _flat("dhN", dhN, 4, cols, dev), dxp, dgp,
+        _flat("dh0", dh0, 4, cols, dev),
         _scan_params(params, xs, gs, ys), wp, wn, _stream(stream, dev)), "lapmix_scan_backward_ws")
 
 
@@ -226,7 +232,7 @@ def lapmix_scan_step(x, g, y, h_in, h_out, params: lapmix_scan_params, slots=Non
     gp, gs = _heads("g", g, size, shape, dev)
     yp, ys = _heads("y", y, size, shape, dev)
     _check(_lib.lapmix_scan_step(
-        xp, gp, _flat("slots", slots, 4, shape[0], dev), _flat("h_in", h_in, 4, pool, dev),
+        xp, gp, _flat("slots", slots, 4, shape[0], dev, _INDEX), _flat("h_in", h_in, 4, pool, dev),
         _flat("h_out", h_out, 4, pool, dev), n_slots, yp, _scan_params(params, xs, gs, ys), _stream(stream, dev)),
         "lapmix_scan_step")
 

@@ -681,6 +681,26 @@ def test_norm_nan_and_infinity_stay_in_their_row():
         assert c.y[0, 2].float().isnan().any() and c.y[0, 4].float().isnan().any()
 
 
+def test_norm_rows_beyond_a_launch():
+    """More rows than one launch's 2^32 lanes take: 67117056 rows of 65 columns, one batch's x repeated
+    (stride 0) 8193 times."""
+    torch = torch_mod()
+    import laplacian_nystr_approximation_amd as L
+    B, N, C = 8193, 8192, 65
+    x = torch.randn(1, 1, N, C, device="cuda").bfloat16().expand(B, 1, N, C)
+    w = torch.randn(C, device="cuda")
+    y = torch.zeros(B, N, C, dtype=torch.bfloat16, device="cuda")
+    p = L.make_norm_params(B=B, H=1, N=N, d=C, x_dtype="bf16", r_dtype="bf16", y_dtype="bf16")
+    L.lapmix_norm_forward(x, w, y, p)
+    one = torch.zeros(1, N, C, dtype=torch.bfloat16, device="cuda")
+    L.lapmix_norm_forward(x[:1], w, one, L.make_norm_params(B=1, H=1, N=N, d=C, x_dtype="bf16", r_dtype="bf16",
+                                                            y_dtype="bf16"))
+    torch.cuda.synchronize()
+    assert one.any()
+    for b in range(0, B, 512):
+        assert (y[b:b + 512] == one).all()
+
+
 def test_norm_in_place_and_optional_outputs():
     """s on top of r, dr on top of ds, and each output of the backward alone."""
     torch = torch_mod()

@@ -66,6 +66,7 @@ def test_struct_layouts():
     (dict(N=0), B.LAPNYS_ERR_INVALID_ARG), (dict(d=0), B.LAPNYS_ERR_INVALID_ARG),
     (dict(dtype=2), B.LAPNYS_ERR_UNSUPPORTED), (dict(dtype=7), B.LAPNYS_ERR_UNSUPPORTED),
     (dict(B=1 << 16, H=1 << 16), B.LAPNYS_ERR_UNSUPPORTED), (dict(B=1 << 15, H=1 << 15, d=4), B.LAPNYS_ERR_UNSUPPORTED),
+    (dict(B=1 << 14, H=1 << 8, d=65), B.LAPNYS_ERR_UNSUPPORTED), (dict(B=1, H=1, N=(1 << 30) + 1), B.LAPNYS_ERR_UNSUPPORTED),
 ])
 def test_scan_params_refused(kw, code):
     p = _scan(**kw)
@@ -120,20 +121,28 @@ def test_scan_buffers_refused():
 
 def test_interleaved_gradients_are_told_from_overlapping_ones():
     """dx and dg as the halves of a [B, N, 2, H, d] buffer pass the overlap check (the call then
-    stops at the missing workspace or an invalid tensor of another kind), a shifted pair does not."""
-    p = _scan()
-    st = (600 * 2 * 3 * 64, 64, 2 * 3 * 64)
+    stops at the missing workspace), a shifted pair does not."""
+    p = _scan(N=640)
+    st = (640 * 2 * 3 * 64, 64, 2 * 3 * 64)
     p.x_stride[:] = st
     p.g_stride[:] = st
-    bad = B.LAPNYS_ERR_INVALID_ARG
+    bad, stops = B.LAPNYS_ERR_INVALID_ARG, B.LAPNYS_ERR_WORKSPACE
     apart = 3 * 64 * 2
-    lib = L.library()
-    assert _bwd(p, dx=5 * A, dg=5 * A + apart - 2) == bad
-    assert _bwd(p, dx=5 * A, dg=5 * A + 64 * 2) == bad  # the next head
-    assert _bwd(p, dx=5 * A, dg=5 * A + 2 * apart) == bad  # the next token
-    # allowed, and refused only for dh0 on top of an input
-    assert _bwd(p, dx=5 * A, dg=5 * A + apart, dh0=A) == bad
-    assert lib.lapnys_status_string(bad)
+    assert L.lapmix_scan_workspace_size(p) > 0
+    assert _bwd(p, dx=5 * A, dg=5 * A + apart - 2, ws=None) == bad
+    assert _bwd(p, dx=5 * A, dg=5 * A + 64 * 2, ws=None) == bad  # the next head
+    assert _bwd(p, dx=5 * A, dg=5 * A + 2 * apart, ws=None) == bad  # the next token
+    assert _bwd(p, dx=5 * A, dg=5 * A + apart, ws=None) == stops
+    assert _bwd(p, dx=5 * A, dg=5 * A - apart, ws=None) == stops
+    # the same for the forward's inputs and output as three parts of one buffer
+    q = _scan(N=640)
+    for st in (q.x_stride, q.g_stride, q.y_stride):
+        st[:] = (640 * 3 * 3 * 64, 64, 3 * 3 * 64)
+    assert _fwd(q, x=A, g=A + apart, y=A + 2 * apart, ws=None) == stops
+    assert _fwd(q, x=A, g=A + apart, y=A + apart, ws=None) == bad
+    # the state carried in place stops at the workspace too
+    assert _fwd(q, h0=7 * A, hN=7 * A, y=4 * A, ws=None) == stops
+    assert _bwd(p, dhN=7 * A, dh0=7 * A, ws=None) == stops
 
 
 def test_step_refusals():
@@ -144,6 +153,7 @@ def test_step_refusals():
                dict(h_out=3 * A + 4), dict(y=3 * A), dict(y=4 * A), dict(slots=4 * A), dict(h_out=A)):
         assert _step(p, **kw) == bad, kw
     assert _step(p, n=1) == B.LAPNYS_ERR_SHAPE
+    assert _step(_scan(B=(1 << 25) + 1, H=1, N=1, d=1), n=1 << 30) == B.LAPNYS_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -218,6 +228,12 @@ def test_binding_checks_tensors():
         L.lapmix_scan_forward_ws(A, 2 * A, 3 * A, p, None, hN=torch.zeros(7))
     with pytest.raises(ValueError, match="states: expected"):
         L.lapmix_scan_forward_ws(A, 2 * A, 3 * A, p, None, states=torch.zeros(7))
+    with pytest.raises(ValueError, match="x: expected .*float16"):
+        L.lapmix_scan_forward_ws(t.half(), t, t, p, None)
+    with pytest.raises(ValueError, match="lengths: expected .*float32"):
+        L.lapmix_scan_forward_ws(A, 2 * A, 3 * A, p, None, lengths=torch.zeros(1))
+    with pytest.raises(ValueError, match="h0: expected .*int32"):
+        L.lapmix_scan_forward_ws(A, 2 * A, 3 * A, p, None, h0=torch.zeros(8, dtype=torch.int32))
     with pytest.raises(ValueError, match="n_slots"):
         L.lapmix_scan_step(A, 2 * A, 3 * A, 4 * A, 5 * A, _scan(N=1))
     with pytest.raises(ValueError, match="slots: expected"):
