@@ -8,21 +8,36 @@
 // (A, S), the lanes' pairs are composed over the wave by lane exchange and over
 // the workgroup through LDS, and with the state before the tile known each lane
 // walks its tokens a second time, in registers, and writes y.  x and g are read
-// once and y is written once: the kernel is bound by HBM.  While a workgroup
-// works on a tile, the loads of its next one are under way.
+// once and y is written once: the kernel is bound by HBM.
 //
 // The state before a tile comes from one of two places.
-//  - Loop form: a workgroup takes all tiles of its columns one after the other.
+//  - Loop form: a workgroup takes all tiles of its columns one after the other;
+//    while it works on one, the loads of the next are under way.
 //  - Chain form, for few columns: several workgroups share the tiles of a group of
-//    columns and take them as they come.  A tile publishes its (A, S), every kFan-th tile also the pair of the last kFan tiles,
-//    every kFan^2-th that of the last kFan^2, and so on, so that a tile composes at
-//    most kFan - 1 pairs of each level.  Which pairs are composed, and in which
-//    order, depends on the tile's place alone: results repeat bit for bit.
+//    columns and take them as they come.  A tile publishes its (A, S), every kFan-th
+//    tile also the pair of the last kFan tiles, every kFan^2-th that of the last
+//    kFan^2, and so on, so that a tile composes at most kFan - 1 pairs of each level.
+//    Which pairs are composed, and in which order, depends on the tile's place
+//    alone: results repeat bit for bit.
 //
 // Waits end: workgroups draw a group's tiles from the group's counter, in order, and
 // finish one before they draw the next, so the lowest unfinished tile is being
-// worked on and waits only for tiles below it, which are finished.  (A counter
-// for each group: one for all of them is a bottleneck, about 15 ns a draw.)
+// worked on and waits only for tiles below it, which are finished.
+//
+// Measured (MI355X, a large copy runs at 5.2 TB/s; forward and backward, the backward
+// with dx and dg): 65536 columns of 1024 tokens in bf16, loop form, 164 us (4.9 TB/s)
+// and 272 us (4.9); in float32 167 (4.8) and 270 (5.0); 4096 columns of 32768 tokens in
+// bf16, chain form, 190 to 200 us (4.0 to 4.2) and 320 us (4.2); 512 columns of 65536 tokens 50
+// and 93 us.  Of the chain form's time about a tenth is the latency of publishing
+// and reading pairs, which three workgroups a CU (two in the backward) do not
+// hide entirely: a fourth does not fit the registers without spilling, and spilled
+// it took 219 us and more in the forward.  What else was tried on the 4096
+// columns, bf16: one counter for all groups 248 us forward (a draw of one address takes
+// about 15 ns, whoever draws); drawing the next tile before this one's wait, with its
+// loads under way during the wait, 250 (others then wait for a tile that is drawn
+// but not begun); 256 tokens a tile 191; 512 lanes a workgroup with 8 channels by 4 tokens a
+// lane 220 forward and 488 backward; gates packed into one register in the backward, 3 waves a SIMD
+// that spill, 376 to 598.
 //
 // The backward pass runs the tiles from the last to the first with r = f dh in
 // the place of h (r_t = f_t (dy_t + r_{t+1})), and recomputes the tile's h from
@@ -36,7 +51,7 @@ namespace lapmix {
 namespace {
 
 constexpr int kFan = 8;      // pairs of a level that make one of the next
-constexpr int kLevels = 5;   // the highest level's pairs stand for kFan^4 tiles
+constexpr int kLevels = 8;   // the highest level's pairs stand for kFan^7 tiles (2^28 tokens)
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
