@@ -91,12 +91,12 @@ def make_norm_params(*, B, H, N, d, x_dtype="f32", r_dtype="f32", y_dtype="f32",
 
 # Decoding steps are a few microseconds long on the GPU, so the checks of a call go by
 # the shortest ways to a tensor's facts and ask for the current device once (``dev``).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _current():
     """Index of the current device; without a GPU, where every tensor is refused as a host tensor, -1."""
-    return torch.cuda.current_device() if _raw_stream and torch.cuda.device_count() else -1
+    return torch.cuda.current_device() if torch.cuda.device_count() else -1
 
 
 def _stream(stream, dev):
