@@ -267,14 +267,17 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(Nor
         for (int o = 1; o < a.group / V; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
         int code[2];
         const bool sure = c >= a.C || codes_of<V>(code, v[k], w[k], m, rstd);
-        double exact = m;
+        // The scale goes by what decides it in this group, not by what others in the wave
+        // make of it: by 32 bits where they hold the maximum.
+        double scaled = m;
         if (!__all(sure)) {
-          exact = c < a.C ? largest<V>(v[k], w[k]) : 0.;
+          double exact = c < a.C ? largest<V>(v[k], w[k]) : 0.;
           for (int o = 1; o < a.group / V; o *= 2) exact = fmax(exact, __shfl_xor(exact, o));
           if (!sure) exact_codes<V>(code, v[k], w[k], exact, rstd);
+          if (!ordinary(m)) scaled = exact;
         }
         if (c < a.C) {
-          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = scale_of(exact, rstd);
+          if (c % a.group == 0) a.scale[(row * a.C + c) / a.group] = scale_of(scaled, rstd);
           put_codes<V>((uint8_t*)a.y + row * a.C + c, code);
         }
       } else if (c < a.C) {

@@ -25,19 +25,23 @@
 // worked on and waits only for tiles below it, which are finished.
 //
 // Measured (MI355X, a large copy runs at 5.2 TB/s; forward and backward, the backward
-// with dx and dg): 65536 columns of 1024 tokens in bf16, loop form, 164 us (4.9 TB/s)
-// and 272 us (4.9); in float32 167 (4.8) and 270 (5.0); 4096 columns of 32768 tokens in
-// bf16, chain form, 190 to 200 us (4.0 to 4.2) and 320 us (4.2); 512 columns of 65536 tokens 50
-// and 93 us.  Of the chain form's time about a tenth is the latency of publishing
-// and reading pairs, which three workgroups a CU (two in the backward) do not
-// hide entirely: a fourth does not fit the registers without spilling, and spilled
-// it took 219 us and more in the forward.  What else was tried on the 4096
-// columns, bf16: one counter for all groups 248 us forward (a draw of one address takes
-// about 15 ns, whoever draws); drawing the next tile before this one's wait, with its
-// loads under way during the wait, 250 (others then wait for a tile that is drawn
-// but not begun); 256 tokens a tile 191; 512 lanes a workgroup with 8 channels by 4 tokens a
-// lane 220 forward and 488 backward; gates packed into one register in the backward, 3 waves a SIMD
-// that spill, 376 to 598.
+// with dx and dg): 131072 columns of 1024 tokens in bf16, loop form, 164 us (4.9 TB/s)
+// and 272 us (4.9); 65536 columns in float32 167 (4.8) and 270 (5.0); 4096 columns of
+// 32768 tokens in bf16, chain form, 190 to 200 us (4.0 to 4.2) and 320 us (4.2); 512
+// columns of 65536 tokens 50 and 93 us.
+//
+// A tile of the chain form takes 9.7 us of a forward workgroup's time: 3.1 until its
+// loads are there, 1.4 for gates and pairs, 3.1 for publishing, waiting and composing
+// (two trips to memory and back), 1.4 for y.  Three workgroups a CU (two in the
+// backward) do not hide all of that, and one more does not fit the registers: where it
+// was made to, it spilled (219 us and more forward, 376 and more backward).  What else
+// was tried on the 4096 columns in bf16: one counter for all groups, 248 us forward (a
+// draw at one address takes about 15 ns, whoever draws); drawing the next tile before
+// this one's wait, with its loads under way during the wait, 250 (others then wait for
+// a tile that is drawn but not begun); drawing it between the wait and y, 188 forward
+// and 308 backward, but 305 instead of 285 where gates are logarithmic; tiles of 256
+// tokens, 191; 512 lanes with 8 channels by 4 tokens each, 220 and 488; u, or h before each
+// token, kept in LDS, 195 to 224 forward.
 //
 // The backward pass runs the tiles from the last to the first with r = f dh in
 // the place of h (r_t = f_t (dy_t + r_{t+1})), and recomputes the tile's h from

@@ -649,6 +649,24 @@ def test_norm_e4m3(rows, H, d, group, r_dtype, x_dtype):
     c.check_forward()
 
 
+@pytest.mark.parametrize("y_dtype,group", [("bf16", 0), ("e4m3", 0), ("e4m3", 16), ("e4m3", 128)])
+@pytest.mark.parametrize("C", [128, 512, 4096])
+def test_norm_rows_do_not_depend_on_their_neighbours(C, y_dtype, group):
+    """A row gives the same bits among 600 others and alone: codes and scales of a group are decided by the
+    group's values, whatever the rest of its wave holds."""
+    torch = torch_mod()
+    c = Norm(600, 1, C, "bf16", "bf16", y_dtype, group)
+    c.forward()
+    torch.cuda.synchronize()
+    p = c.L.make_norm_params(B=1, H=1, N=1, d=C, x_dtype="bf16", r_dtype="bf16", y_dtype=y_dtype, eps=c.eps, group=group)
+    for i in range(0, 600, 7):
+        y, s = torch.empty_like(c.y[:, i]), torch.empty_like(c.s[:, i])
+        scale = None if c.scale is None else torch.empty_like(c.scale[:, i])
+        c.L.lapmix_norm_forward(c.x[:, :, i:i + 1], c.w, y, p, r=c.r[:, i], s=s, scale=scale)
+        assert torch.equal(y.view(torch.uint8), c.y[:, i].contiguous().view(torch.uint8))
+        assert scale is None or torch.equal(scale, c.scale[:, i])
+
+
 def test_norm_rows_of_zeros_and_extremes():
     """A row of zeros, rows of tiny and of large values, and e4m3 of all of them."""
     torch = torch_mod()
