@@ -54,8 +54,11 @@ namespace lapmix {
 
 namespace {
 
-constexpr int kFan = 8;      // pairs of a level that make one of the next
-constexpr int kLevels = 8;   // the highest level's pairs stand for kFan^7 tiles (2^28 tokens)
+// Pairs of a level that make one of the next.  (4096 columns of 32768 bf16 tokens, forward
+// and backward: 8 pairs 204 and 318 us, 16 201 and 311, 32 201 and 311 to 319; 512 columns
+// of 65536: 51.6 and 94.7, 52.8 and 94.1, 53.7 and 93.9.)
+constexpr int kFan = 16;
+constexpr int kLevels = 6;  // the highest level's pairs stand for kFan^5 tiles (2^27 tokens)
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
@@ -129,7 +132,7 @@ long long chain_layout(int ntiles, long long columns, long long groups, long lon
 // lanes take part: each waits for a few of a column's pairs (SLOTS lanes a column).
 template <int WIDTH>
 __device__ __forceinline__ Pair chain_before(const Chain& c, int p, int last, uint32_t base, Pair own) {
-  constexpr int SLOTS = kThreads / WIDTH, EACH = kFan / SLOTS, FIRST = 3;
+  constexpr int SLOTS = kThreads / WIDTH, EACH = kFan / SLOTS, FIRST = 2;
   __shared__ Pair parts[kLevels][SLOTS][WIDTH];
   const int slot = threadIdx.x / WIDTH, lane = threadIdx.x % WIDTH;
   const bool on = base + lane < (uint64_t)c.columns;

@@ -224,10 +224,10 @@ def test_scan_remembers_over_the_whole_sequence():
     c.check()
 
 
-@pytest.mark.parametrize("N", [5000, 70000, 700001])
+@pytest.mark.parametrize("N", [5000, 70000, 700001, 8500007])
 def test_scan_counts_exactly_over_long_sequences(N):
     """Gates of 1 and 0 and whole inputs: states are counts since the last reset, exact in float32, and
-    so are the gradients; 700001 tokens take pairs of every level (4096 tiles are 524288 tokens)."""
+    so are the gradients; 700001 tokens take pairs of four levels (4096 tiles are 524288 tokens), 8500007 of five."""
     torch = torch_mod()
     d = 4
     gen = torch.Generator().manual_seed(N)
