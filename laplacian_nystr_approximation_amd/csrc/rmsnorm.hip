@@ -204,6 +204,13 @@ struct Place {
   }
 };
 
+// Offset of column c in a token of x or dx.
+__device__ __forceinline__ int64_t in_heads(const NormArgs& a, int c) {
+  if (a.H == 1) return c;
+  const int h = c / a.d;
+  return h * a.xs.h + (c - h * a.d);
+}
+
 // X, R, Y: types of x, r and s, and y.  CH chunks of V columns a lane.
 template <typename X, typename R, typename Y, int V, int TPR, int CH>
 __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(NormArgs a) {
@@ -223,8 +230,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_forward_kernel(Nor
   for (int k = 0; k < CH; ++k) {
     const int c = (k * at.lanes + at.lane) * V;
     if (c < a.C) {
-      const int h = c / a.d;
-      xr[k] = get<V>(x + h * a.xs.h + (c - h * a.d));
+      xr[k] = get<V>(x + in_heads(a, c));
       if (a.r) rr[k] = get<V>((const R*)a.r + row * a.C + c);
     }
   }
@@ -318,10 +324,15 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
     Raw<R, V> s[CH], ds[CH];
     Raw<Y, V> dy[CH];
   };
+  // With many chunks columns are worked out anew for each row: kept over the rows, the
+  // addresses would not leave room for the row itself (8192 float32 rows of 8191 columns:
+  // 433 us, anew 264; with four chunks it costs a tenth).
+  int lane = at.lane;
   auto load = [&](long long row, Row& r) {
+    if constexpr (CH > 4) asm volatile("" : "+v"(lane));
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = (k * at.lanes + at.lane) * V;
+      const int c = (k * at.lanes + lane) * V;
       if (row < a.rows && c < a.C) {
         r.s[k] = get<V>((const R*)a.s + row * a.C + c);
         r.dy[k] = get<V>((const Y*)a.dy + row * a.C + c);
@@ -330,7 +341,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
     }
   };
   // The next row's loads are under way during a row where registers allow.
-  constexpr bool AHEAD = V * CH <= 8;
+  constexpr bool AHEAD = V * CH <= 8 && CH <= 4;
   Row next;
   long long row = (long long)blockIdx.x * at.rows + at.row;
   if (AHEAD) load(row, next);
@@ -343,7 +354,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
     float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < CH; ++k)
-      if (on && (k * at.lanes + at.lane) * V < a.C)
+      if (on && (k * at.lanes + lane) * V < a.C)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           sums[0] += r.s[k][i] * r.s[k][i];
@@ -358,7 +369,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
     X* dx = (X*)a.dx + b * a.xs.b + n * a.xs.n;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = (k * at.lanes + at.lane) * V;
+      const int c = (k * at.lanes + lane) * V;
       if (c >= a.C) continue;
       float g[V];
 #pragma unroll
@@ -369,8 +380,7 @@ __global__ __launch_bounds__(TPR ? kNarrow : kWide) void norm_backward_kernel(No
       }
       if (a.dr) put<R, V>((R*)a.dr + row * a.C + c, g);
       if (a.dx) {
-        const int h = c / a.d;
-        put<X, V>(dx + h * a.xs.h + (c - h * a.d), g);
+        put<X, V>(dx + in_heads(a, c), g);
       }
     }
   }
@@ -449,7 +459,7 @@ Shape shape_of(int C, bool vec) {
     return wide(chunks <= 128 ? 1 : 2);
   }
   if (chunks <= 64) return {v, 64, 1, kNarrow};
-  return wide(chunks <= 4096 ? 4 : 16);
+  return wide(chunks <= 4096 ? 4 : chunks <= 8192 ? 8 : 16);
 }
 
 template <typename F>
@@ -460,7 +470,8 @@ void with_shape(const Shape& s, F f) {
     return s.ch == 1 ? f(Int<8>(), Int<0>(), Int<1>()) : f(Int<8>(), Int<0>(), Int<2>());
   }
   if (s.tpr == 64) return f(Int<1>(), Int<64>(), Int<1>());
-  return s.ch == 4 ? f(Int<1>(), Int<0>(), Int<4>()) : f(Int<1>(), Int<0>(), Int<16>());
+  if (s.ch == 4) return f(Int<1>(), Int<0>(), Int<4>());
+  return s.ch == 8 ? f(Int<1>(), Int<0>(), Int<8>()) : f(Int<1>(), Int<0>(), Int<16>());
 }
 
 template <typename F>
