@@ -490,10 +490,11 @@ void with_types(const NormArgs& a, F f) {
 // Workgroups of the backward pass: about 16 waves to each of the 256 CUs, so that
 // the parts of dw stay small beside the rows, and four rows or more for each.  (16384
 // rows of 2560 bf16 columns, 5 waves a row: 114 us with 256 workgroups, 86 with 512,
-// 88 with 1024, 97 with 2048; 4096 rows of 1024, 2 waves: 21.7, 16.1, 14.6, 17.3.)
+// 88 with 1024, 97 with 2048; 4096 rows of 1024, 2 waves: 21.7, 16.1, 14.6, 17.3; 65536
+// float32 rows of 67, 1 wave: 71 with 1024, 46 with 2048, 39 with 4096.)
 static int norm_groups(long long rows, const Shape& shape) {
   const long long n = (rows + 4 * shape.rows() - 1) / (4 * shape.rows());
-  const int waves = shape.block / 64, most = waves > 4 ? 512 : 1024;
+  const int waves = shape.block / 64, most = waves > 4 ? 512 : waves > 1 ? 1024 : 4096;
   return (int)(n < most ? n : most);
 }
 
