@@ -11,7 +11,7 @@
 // Measured (MI355X, a large copy runs at 5.2 TB/s): 32768 rows of 2048 in bf16 91 us
 // forward (5.9 TB/s) and 128 us backward with dr, dx and dw (5.2); 16384 rows of 4096
 // to e4m3 86 us with a scale every 128 columns (5.5) and 97 us with one a row, where
-// all of the row's waves have to meet twice; 16384 rows of 2560, forward and backward of a
+// all of the row's waves have to meet a second time; 16384 rows of 2560, forward and backward of a
 // training step, 144 us.
 #include <type_traits>
 
