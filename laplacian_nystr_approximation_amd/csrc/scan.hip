@@ -27,8 +27,8 @@
 // Measured (MI355X, a large copy runs at 5.2 TB/s; forward and backward, the backward
 // with dx and dg): 131072 columns of 1024 tokens in bf16, loop form, 164 us (4.9 TB/s)
 // and 272 us (4.9); 65536 columns in float32 167 (4.8) and 270 (5.0); 4096 columns of
-// 32768 tokens in bf16, chain form, 190 to 200 us (4.0 to 4.2) and 311 us (4.3); 512
-// columns of 65536 tokens 52 and 94 us.
+// 32768 tokens in bf16, chain form, 190 to 200 us (4.0 to 4.2) and 311 to 327 us (4.1
+// to 4.3); 512 columns of 65536 tokens 52 and 94 us.
 //
 // A tile of the chain form takes 9.7 us of a forward workgroup's time: 3.1 until its
 // loads are there, 1.4 for gates and pairs, 3.1 for publishing, waiting and composing
